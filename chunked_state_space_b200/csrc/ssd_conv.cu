@@ -1,0 +1,297 @@
+// Short causal depthwise convolution with bias and SiLU, for prompts and for
+// single tokens:
+//   y[b,t,c] = act(bias[c] + sum_{k<W} w[c,k] x[b, t-(W-1)+k, c])
+// with the inputs before the first token taken from a cached state (or 0).
+//
+// Bound by HBM: each element is read once and written once, against about a
+// dozen fp32 operations and two special-function ones (e^-v and a reciprocal).
+// A thread owns 16 bytes of channels (one element where rows are not 16-byte
+// aligned) and a run of consecutive tokens, and keeps the last W-1 inputs in
+// registers, so a tap costs no further load; only the W-1 rows before a run
+// are read twice.  Eight rows are loaded before the first is used.
+#include "ssd_rows.cuh"
+
+namespace ssd {
+namespace conv {
+
+constexpr int THREADS = 128;
+constexpr int AHEAD = 8;  // rows in flight per thread
+
+template <typename T>
+struct Args {
+  Rows<const T> x;
+  Rows<T> y;
+  const float* weight;
+  const float* bias;
+  const T* init;
+  T* final_state;
+  const int32_t* lengths;
+  int64_t B, L, C;
+  uint32_t nvec, ntiles, total;
+  int tile;  // tokens per thread, a multiple of AHEAD
+};
+
+template <int W, int VEC, bool SILU>
+struct Taps {
+  float w[W][VEC], b[VEC];
+  __device__ __forceinline__ void load(const float* weight, const float* bias, int64_t c) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][i] = weight[(c + i) * W + k];
+      b[i] = bias ? bias[c + i] : 0.f;
+    }
+  }
+  // old[0] is the oldest of the W-1 inputs before `in`
+  template <typename T>
+  __device__ __forceinline__ Pack<T, VEC> apply(const float (&old)[W - 1][VEC], const float (&in)[VEC]) const {
+    Pack<T, VEC> out;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      float acc = b[i];
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], old[k][i], acc);
+      acc = fmaf(w[W - 1][i], in[i], acc);
+      out.v[i] = from_f32<T>(SILU ? silu(acc) : acc);
+    }
+    return out;
+  }
+};
+
+template <typename T, int W, int VEC, bool SILU>
+__global__ void __launch_bounds__(THREADS) k_conv_fwd(const Args<T> a) {
+  const uint32_t idx = blockIdx.x * THREADS + threadIdx.x;
+  if (idx >= a.total) return;
+  const uint32_t r = idx / a.nvec;
+  const int64_t c = (int64_t)(idx - r * a.nvec) * VEC;
+  const uint32_t b32 = r / a.ntiles, tile = r - b32 * a.ntiles;
+  const int64_t b = b32;
+  const int64_t len = row_length(a.lengths, b, a.L);
+  const int64_t t0 = (int64_t)tile * a.tile;
+  if (t0 >= len && tile != 0) return;
+  const int64_t t1 = t0 + a.tile < len ? t0 + a.tile : len;
+  float old[W - 1][VEC];  // the W-1 inputs before the next token, oldest first
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    Pack<T, VEC> v;
+    if (tile != 0) {
+      v = load_pack<T, VEC>(a.x.row(b, t0 - (W - 1) + k) + c);
+    } else if (a.init) {
+      v = load_pack<T, VEC>(a.init + (b * (W - 1) + k) * a.C + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v.v[i] = from_f32<T>(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) old[k][i] = to_f32(v.v[i]);
+  }
+  if (tile == 0 && a.final_state) {
+    // The thread that read these channels of init_state writes their final
+    // state, so that both may be one buffer.
+    Pack<T, VEC> last[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const int64_t t = len - (W - 1) + k;
+      if (t >= 0) {
+        last[k] = load_pack<T, VEC>(a.x.row(b, t) + c);
+      } else {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+          if (j == (int)(t + W - 1)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) last[k].v[i] = from_f32<T>(old[j][i]);
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_pack<T, VEC>(a.final_state + (b * (W - 1) + k) * a.C + c, last[k]);
+  }
+  Taps<W, VEC, SILU> taps;
+  taps.load(a.weight, a.bias, c);
+  for (int64_t t = t0; t < t1; t += AHEAD) {
+    Pack<T, VEC> in[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (t + j < t1) in[j] = load_pack<T, VEC>(a.x.row(b, t + j) + c);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (t + j < t1) {
+        float cur[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) cur[i] = to_f32(in[j].v[i]);
+        store_pack<T, VEC>(a.y.row(b, t + j) + c, taps.template apply<T>(old, cur));
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+          for (int k = 0; k + 1 < W - 1; ++k) old[k][i] = old[k + 1][i];
+          old[W - 2][i] = cur[i];
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int W, int VEC, bool SILU>
+__global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, int64_t xbs, const float* weight,
+                                                       const float* bias, T* state, T* __restrict__ y, int64_t ybs,
+                                                       int64_t C, uint32_t nvec, uint32_t total) {
+  const uint32_t idx = blockIdx.x * THREADS + threadIdx.x;
+  if (idx >= total) return;
+  const uint32_t b32 = idx / nvec;
+  const int64_t b = b32, c = (int64_t)(idx - b32 * nvec) * VEC;
+  T* st = state + b * (W - 1) * C + c;
+  Pack<T, VEC> seen[W];
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) seen[k] = load_pack<T, VEC>(st + k * C);
+  seen[W - 1] = load_pack<T, VEC>(x + b * xbs + c);
+  Taps<W, VEC, SILU> taps;
+  taps.load(weight, bias, c);
+  float old[W - 1][VEC], cur[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) old[k][i] = to_f32(seen[k].v[i]);
+    cur[i] = to_f32(seen[W - 1].v[i]);
+  }
+  store_pack<T, VEC>(y + b * ybs + c, taps.template apply<T>(old, cur));
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) store_pack<T, VEC>(st + k * C, seen[k + 1]);
+}
+
+// Tokens per thread: as many as leave every SM about 1024 threads (the rows
+// before a run are read twice, so longer runs read less), at most 64.
+inline int tile_tokens(int64_t B, int64_t L, int64_t nvec) {
+  int tile = 64;
+  while (tile > AHEAD && B * nvec * ceil_div(L, tile) < 148 * 1024) tile /= 2;
+  return tile;
+}
+
+template <typename T, int W, int VEC>
+cudaError_t launch(const Args<T>& a0, bool use_silu, cudaStream_t st) {
+  Args<T> a = a0;
+  const int64_t nvec = a.C / VEC;
+  int64_t tile = tile_tokens(a.B, a.L, nvec);
+  while (a.B * nvec * ceil_div(a.L, tile) > 0x7fff0000) tile *= 2;  // thread indices stay below 2^31
+  a.tile = (int)tile;
+  a.nvec = (uint32_t)nvec;
+  a.ntiles = (uint32_t)ceil_div(a.L, tile);
+  a.total = (uint32_t)(a.B * nvec * a.ntiles);
+  const unsigned blocks = (a.total + THREADS - 1) / THREADS;
+  if (use_silu)
+    k_conv_fwd<T, W, VEC, true><<<blocks, THREADS, 0, st>>>(a);
+  else
+    k_conv_fwd<T, W, VEC, false><<<blocks, THREADS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int W, int VEC>
+cudaError_t launch_step(const ssd_conv_dims* d, const void* x, int64_t xbs, const float* weight, const float* bias,
+                        void* state, void* y, int64_t ybs, cudaStream_t st) {
+  const uint32_t nvec = (uint32_t)(d->channels / VEC), total = (uint32_t)(d->batch * nvec);
+  const unsigned blocks = (total + THREADS - 1) / THREADS;
+  if (d->flags & SSD_CONV_SILU)
+    k_conv_step<T, W, VEC, true><<<blocks, THREADS, 0, st>>>((const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs,
+                                                             d->channels, nvec, total);
+  else
+    k_conv_step<T, W, VEC, false><<<blocks, THREADS, 0, st>>>((const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs,
+                                                              d->channels, nvec, total);
+  return cudaGetLastError();
+}
+
+// f(T, W, VEC) for the call's type, width and alignment.
+template <typename F>
+cudaError_t dispatch(int io, int64_t width, bool vec, F&& f) {
+  auto with_width = [&](auto t, auto v) {
+    switch (width) {
+      case 2: return f(t, std::integral_constant<int, 2>(), v);
+      case 3: return f(t, std::integral_constant<int, 3>(), v);
+      default: return f(t, std::integral_constant<int, 4>(), v);
+    }
+  };
+  if (io == SSD_BF16)
+    return vec ? with_width(__nv_bfloat16(), std::integral_constant<int, 8>())
+               : with_width(__nv_bfloat16(), std::integral_constant<int, 1>());
+  return vec ? with_width(float(), std::integral_constant<int, 4>())
+             : with_width(float(), std::integral_constant<int, 1>());
+}
+
+ssd_status validate(const ssd_conv_dims* d, int64_t seqlen) {
+  if (!d) return SSD_ERR_INVALID_ARG;
+  if (d->flags & ~SSD_CONV_SILU) return SSD_ERR_INVALID_ARG;
+  if (d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) return SSD_ERR_DTYPE;
+  if (d->batch < 1 || seqlen < 1 || d->channels < 1 || d->width < 1) return SSD_ERR_SHAPE;
+  if (d->width < 2 || d->width > 4) return SSD_ERR_UNSUPPORTED;
+  // thread indices stay below 2^31 (a run of tokens per thread can grow, a row cannot)
+  if (d->channels > (int64_t(1) << 24) || d->batch > (int64_t(1) << 24) || d->batch * d->channels > 0x7fff0000 ||
+      seqlen > (int64_t(1) << 31))
+    return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+
+}  // namespace conv
+}  // namespace ssd
+
+extern "C" ssd_status ssd_conv_fwd(const ssd_conv_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
+                                   const float* weight, const float* bias, const void* init_state,
+                                   const int32_t* lengths, void* y, int64_t y_bstride, int64_t y_tstride,
+                                   void* final_state, void* stream) {
+  using namespace ssd;
+  ssd_status s = conv::validate(d, d ? d->seqlen : 1);
+  if (s != SSD_OK) return s;
+  if (!x || !weight || !y) return SSD_ERR_INVALID_ARG;
+  const int64_t B = d->batch, L = d->seqlen, C = d->channels, W = d->width;
+  const size_t es = io_bytes(d->io_dtype);
+  const RowArg rx{x, x_bstride, x_tstride, C}, ry{y, y_bstride, y_tstride, C};
+  const RowArg ri{init_state, (W - 1) * C, C, C}, rf{final_state, (W - 1) * C, C, C};
+  if ((s = check_rows(rx, B, L, es, false)) != SSD_OK || (s = check_rows(ry, B, L, es, true)) != SSD_OK) return s;
+  if (check_rows(ri, B, W - 1, es, false) != SSD_OK || check_rows(rf, B, W - 1, es, false) != SSD_OK ||
+      !f32_aligned(weight) || !f32_aligned(bias) || !f32_aligned(lengths))
+    return SSD_ERR_ALIGN;
+  const Span sx{x, row_extent(rx, B, L, es)}, sy{y, row_extent(ry, B, L, es)}, sw{weight, sizeof(float) * C * W},
+      sb{bias, sizeof(float) * C}, si{init_state, es * B * (W - 1) * C}, sl{lengths, sizeof(int32_t) * B},
+      sf{final_state, es * B * (W - 1) * C};
+  for (const Span& in : {sx, sw, sb, sl})
+    if (spans_meet(sy, in) || spans_meet(sf, in)) return SSD_ERR_INVALID_ARG;
+  if (spans_meet(sy, si) || spans_meet(sy, sf) || (final_state != init_state && spans_meet(sf, si)))
+    return SSD_ERR_INVALID_ARG;
+  const bool vec = rows_on_16(rx, B, L, es) && rows_on_16(ry, B, L, es) && rows_on_16(ri, B, W - 1, es) &&
+                   rows_on_16(rf, B, W - 1, es);
+  return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
+    using T = decltype(t);
+    conv::Args<T> a{};
+    a.x = Rows<const T>{(const T*)x, x_bstride, x_tstride};
+    a.y = Rows<T>{(T*)y, y_bstride, y_tstride};
+    a.weight = weight;
+    a.bias = bias;
+    a.init = (const T*)init_state;
+    a.final_state = (T*)final_state;
+    a.lengths = lengths;
+    a.B = B;
+    a.L = L;
+    a.C = C;
+    return conv::launch<T, w.value, v.value>(a, (d->flags & SSD_CONV_SILU) != 0, static_cast<cudaStream_t>(stream));
+  }));
+}
+
+extern "C" ssd_status ssd_conv_step(const ssd_conv_dims* d, const void* x, int64_t x_bstride, const float* weight,
+                                    const float* bias, void* state, void* y, int64_t y_bstride, void* stream) {
+  using namespace ssd;
+  ssd_status s = conv::validate(d, 1);
+  if (s != SSD_OK) return s;
+  if (!x || !weight || !state || !y) return SSD_ERR_INVALID_ARG;
+  const int64_t B = d->batch, C = d->channels, W = d->width;
+  const size_t es = io_bytes(d->io_dtype);
+  const RowArg rx{x, x_bstride, 0, C}, ry{y, y_bstride, 0, C}, rs{state, (W - 1) * C, C, C};
+  if ((s = check_rows(rx, B, 1, es, false)) != SSD_OK || (s = check_rows(ry, B, 1, es, true)) != SSD_OK) return s;
+  if (check_rows(rs, B, W - 1, es, false) != SSD_OK || !f32_aligned(weight) || !f32_aligned(bias)) return SSD_ERR_ALIGN;
+  const Span sx{x, row_extent(rx, B, 1, es)}, sy{y, row_extent(ry, B, 1, es)}, sw{weight, sizeof(float) * C * W},
+      sb{bias, sizeof(float) * C}, ss{state, es * B * (W - 1) * C};
+  for (const Span& in : {sx, sw, sb})
+    if (spans_meet(sy, in) || spans_meet(ss, in)) return SSD_ERR_INVALID_ARG;
+  if (spans_meet(sy, ss)) return SSD_ERR_INVALID_ARG;
+  const bool vec = rows_on_16(rx, B, 1, es) && rows_on_16(ry, B, 1, es) && rows_on_16(rs, B, W - 1, es);
+  return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
+    return conv::launch_step<decltype(t), w.value, v.value>(d, x, x_bstride, weight, bias, state, y, y_bstride,
+                                                            static_cast<cudaStream_t>(stream));
+  }));
+}

@@ -30,7 +30,8 @@ EXPORTED = ["ssd_status_string", "ssd_version", "ssd_scan_workspace_size", "ssd_
             "ssd_selftest_timeout", "ssd_scan_fwd_host", "ssd_scan_fwd_host_workspace_size",
             "ssd_scan_fwd_strided", "ssd_selftest_carry_timeout", "ssd_scan_fwd_vdecay",
             "ssd_selftest_set_segments", "ssd_selftest_set_split", "ssd_selftest_set_step_chunks",
-            "ssd_scan_fwd_normed"]
+            "ssd_scan_fwd_normed", "ssd_conv_fwd", "ssd_conv_step", "ssd_selective_fwd", "ssd_selective_step",
+            "ssd_rmsnorm_gated"]
 
 
 class SSDError(RuntimeError):
@@ -43,6 +44,22 @@ class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
                 ("chunk", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class ConvDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class SelectiveDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("features", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -93,6 +110,14 @@ def lib() -> ctypes.CDLL:
         "ssd_selftest_set_step_chunks": (ctypes.c_int, [ctypes.c_int]),
         "ssd_scan_fwd_normed": (ctypes.c_int, [D, _P, _P, ctypes.c_float] + [_P] * 10),
         "ssd_scan_fwd_vdecay": (ctypes.c_int, [D] + [_P] * 10),
+        "ssd_conv_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+        "ssd_conv_step": (ctypes.c_int, [_P, _P, _I64, _P, _P, _P, _P, _I64, _P]),
+        "ssd_selective_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P,
+                                             _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+        "ssd_selective_step": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P,
+                                              _I64, _P]),
+        "ssd_rmsnorm_gated": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I64,
+                                             _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -389,6 +414,194 @@ def ssd_step(x, dt, A, Bm, Cm, state, D=None, y=None, stream=None, input_dt: boo
     _check(lib().ssd_step(ctypes.byref(dims), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(state),
                           _ptr(y), _stream(stream)), "ssd_step")
     return y
+
+
+# ---- the layer around and beside the scan -------------------------------------------------
+
+def _rows(x: torch.Tensor, shape, *ts):
+    """Checks the io tensors of a call beside its first, `x`: each None or of
+    `shape`, of x's dtype, on x's device, and with dense channels (as x itself)."""
+    dev, dtype = x.device, x.dtype
+    if dev.type != "cuda":
+        raise SSDError(1, "tensors must be on a CUDA device")
+    for t in (x,) + ts:
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise SSDError(2, f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise SSDError(3, f"expected {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise SSDError(1, "tensors on different devices")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise SSDError(2, "each token's channels must be dense")
+
+
+def _whole(x: torch.Tensor, dtype, *pairs):
+    """Checks contiguous tensors (parameters, states): pairs of (tensor or None, shape)."""
+    for t, shape in pairs:
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise SSDError(2, f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise SSDError(3, f"expected {dtype}, got {t.dtype}")
+        if t.device != x.device:
+            raise SSDError(1, "tensors on different devices")
+        if not t.is_contiguous():
+            raise SSDError(1, "tensors must be contiguous")
+
+
+def _groups(x: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor):
+    """(G, N) of the B and C that go with x ([..., C] to [..., G, N])."""
+    if Bm.dim() != x.dim() + 1 or Bm.shape[:-2] != x.shape[:-1] or Cm.shape != Bm.shape:
+        raise SSDError(2, f"B and C must be {tuple(x.shape[:-1])} + (G, N)")
+    if Bm.dtype != x.dtype or Cm.dtype != x.dtype:
+        raise SSDError(3, f"expected {x.dtype}, got {Bm.dtype} and {Cm.dtype}")
+    if Bm.device != x.device or Cm.device != x.device:
+        raise SSDError(1, "tensors on different devices")
+    G, N = Bm.shape[-2:]
+    sb, sc = Bm.stride(), Cm.stride()
+    if sb != sc and any(n > 1 and i != j for n, i, j in zip(Bm.shape, sb, sc)):
+        raise SSDError(2, "B and C must have the same strides")
+    if (N > 1 and sb[-1] != 1) or (G > 1 and sb[-2] != N):
+        raise SSDError(2, "each token's groups must be dense")
+    return G, N
+
+
+def _call(name: str, x: torch.Tensor, stream, *args):
+    """One entry point on x's device and `stream` (default: that device's current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    fn = getattr(_lib or lib(), name)
+    if x.device.index == torch.cuda.current_device():
+        s = fn(*args, handle)
+    else:
+        with torch.cuda.device(x.device):
+            s = fn(*args, handle)
+    if s != 0:
+        _check(s, name)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _at3(t: Optional[torch.Tensor]):
+    """Pointer, batch stride and token stride of a [B, L, ...] tensor."""
+    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _at2(t: Optional[torch.Tensor]):
+    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+
+def _new_rows(x: torch.Tensor, lengths):
+    # rows behind a padded sequence are not written: zeros there, not what memory held
+    make = torch.empty if lengths is None else torch.zeros
+    return make(x.shape, dtype=x.dtype, device=x.device)
+
+
+def ssd_conv_fwd(x, weight, bias=None, init_state=None, lengths=None, silu: bool = True, y=None, final_state=None,
+                 stream=None, want_final: bool = True):
+    """Short causal depthwise convolution over x [B,L,C] (any batch and token strides), weight [C,W] f32,
+    bias [C] f32, then SiLU (silu=False: none).  init_state [B,W-1,C] holds the inputs before the first
+    token (None: zeros); lengths [B] int32 the tokens of each sequence of a padded batch.
+    Returns (y, final_state [B,W-1,C] or None); final_state may be init_state itself.  A y given by the
+    caller keeps its rows behind each sequence; one made here has zeros there."""
+    if x.dim() != 3 or weight.dim() != 2:
+        raise SSDError(2, "x must be [B,L,C] and weight [C,W]")
+    Bz, L, C = x.shape
+    W = weight.shape[1]
+    _rows(x, x.shape, y)
+    _whole(x, torch.float32, (weight, (C, W)), (bias, (C,)))
+    _whole(x, x.dtype, (init_state, (Bz, W - 1, C)), (final_state, (Bz, W - 1, C)))
+    _whole(x, torch.int32, (lengths, (Bz,)))
+    dims = ConvDims(Bz, L, C, W, _io_code(x), int(silu))
+    if y is None:
+        y = _new_rows(x, lengths)
+    if final_state is None and want_final:
+        final_state = torch.empty((Bz, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+    _call("ssd_conv_fwd", x, stream, ctypes.byref(dims), *_at3(x), _at(weight), _at(bias), _at(init_state),
+          _at(lengths), *_at3(y), _at(final_state))
+    return y, final_state
+
+
+def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream=None):
+    """One token of the convolution: x [B,C], state [B,W-1,C] (the last inputs, shifted by x in place).
+    Returns y [B,C]."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise SSDError(2, "x must be [B,C] and weight [C,W]")
+    Bz, C = x.shape
+    W = weight.shape[1]
+    _rows(x, x.shape, y)
+    _whole(x, torch.float32, (weight, (C, W)), (bias, (C,)))
+    _whole(x, x.dtype, (state, (Bz, W - 1, C)))
+    dims = ConvDims(Bz, 1, C, W, _io_code(x), int(silu))
+    if y is None:
+        y = torch.empty((Bz, C), dtype=x.dtype, device=x.device)
+    _call("ssd_conv_step", x, stream, ctypes.byref(dims), *_at2(x), _at(weight), _at(bias), _at(state), *_at2(y))
+    return y
+
+
+def ssd_selective_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state=None, lengths=None,
+                      softplus: bool = True, y=None, final_state=None, stream=None, want_final: bool = True):
+    """The selective scan with a step per channel: x, dt, z [B,L,C], Bm, Cm [B,L,G,N] (any batch and token
+    strides, one pair for Bm and Cm), A [C,N], D, dt_bias [C] f32; the step is softplus(dt + dt_bias)
+    (softplus=False: dt + dt_bias), y is gated by silu(z) where z is given.  init_state [B,C,N] f32
+    (None: zeros), lengths [B] int32 as in ssd_conv_fwd.  Returns (y, final_state [B,C,N] or None);
+    final_state may be init_state itself."""
+    if x.dim() != 3:
+        raise SSDError(2, "x must be [B,L,C]")
+    Bz, L, C = x.shape
+    _rows(x, x.shape, dt, z, y)
+    G, N = _groups(x, Bm, Cm)
+    _whole(x, torch.float32, (A, (C, N)), (D, (C,)), (dt_bias, (C,)), (init_state, (Bz, C, N)),
+           (final_state, (Bz, C, N)))
+    _whole(x, torch.int32, (lengths, (Bz,)))
+    dims = SelectiveDims(Bz, L, C, N, G, _io_code(x), int(softplus))
+    if y is None:
+        y = _new_rows(x, lengths)
+    if final_state is None and want_final:
+        final_state = torch.empty((Bz, C, N), dtype=torch.float32, device=x.device)
+    _call("ssd_selective_fwd", x, stream, ctypes.byref(dims), *_at3(x), *_at3(dt), _at(A), _at(Bm), *_at3(Cm),
+          _at(D), *_at3(z), _at(dt_bias), _at(init_state), _at(lengths), *_at3(y), _at(final_state))
+    return y, final_state
+
+
+def ssd_selective_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, softplus: bool = True, y=None,
+                       stream=None):
+    """One token of the selective scan: x, dt, z [B,C], Bm, Cm [B,G,N], state [B,C,N] f32 (updated in
+    place).  Returns y [B,C]."""
+    if x.dim() != 2:
+        raise SSDError(2, "x must be [B,C]")
+    Bz, C = x.shape
+    _rows(x, x.shape, dt, z, y)
+    G, N = _groups(x, Bm, Cm)
+    _whole(x, torch.float32, (A, (C, N)), (D, (C,)), (dt_bias, (C,)), (state, (Bz, C, N)))
+    dims = SelectiveDims(Bz, 1, C, N, G, _io_code(x), int(softplus))
+    if y is None:
+        y = torch.empty((Bz, C), dtype=x.dtype, device=x.device)
+    _call("ssd_selective_step", x, stream, ctypes.byref(dims), *_at2(x), *_at2(dt), _at(A), _at(Bm), *_at2(Cm),
+          _at(D), *_at2(z), _at(dt_bias), _at(state), *_at2(y))
+    return y
+
+
+def ssd_rmsnorm_gated(x, z=None, weight=None, eps: float = 1e-5, ngroups: int = 1, out=None, stream=None):
+    """out = weight u / sqrt(mean(u^2) + eps) with u = x silu(z) (u = x without z), the mean over each of
+    `ngroups` runs of features; x, z [B,L,F] or [B,F] with any row strides, weight [F] f32.  out may be x."""
+    if x.dim() not in (2, 3):
+        raise SSDError(2, "x must be [B,L,F] or [B,F]")
+    F = x.shape[-1]
+    _rows(x, x.shape, z, out)
+    _whole(x, torch.float32, (weight, (F,)))
+    dims = NormDims(x.shape[0], x.shape[1] if x.dim() == 3 else 1, F, int(ngroups), _io_code(x), 0)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    at = _at3 if x.dim() == 3 else (lambda t: _at2(t) + (0,))
+    _call("ssd_rmsnorm_gated", x, stream, ctypes.byref(dims), *at(x), *at(z), _at(weight), float(eps), *at(out))
+    return out
 
 
 def ssd_read_device_status(stream=None) -> int:

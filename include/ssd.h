@@ -397,6 +397,130 @@ ssd_status ssd_scan_fwd_vdecay(const ssd_dims* d, const void* x, const float* dt
                                float* final_state, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Around and beside the scan: what else a selective state-space layer computes
+ * in a forward pass, for prompts and for single tokens.
+ *
+ * Conventions of these entry points, beside those above:
+ *  - Activations are rows of dense channels: element (b, t, c) of a tensor `v`
+ *    lies at v + b*v_bstride + t*v_tstride + c, strides in elements, so a
+ *    slice of a projection's output is passed as it is.  A stride of a
+ *    dimension of size 1 is not looked at.  Inputs take any stride >= 0 (0
+ *    repeats a row); the rows of an output must not overlap (SSD_ERR_SHAPE).
+ *  - Alignment: the element's own (2 or 4 bytes; else SSD_ERR_ALIGN).  Rows
+ *    that start on 16 bytes are read faster.
+ *  - Parameters (weights, A, D, biases) are f32 and contiguous, io tensors are
+ *    f32 or bf16, and every sum, statistic and scan state is f32.
+ *  - lengths (int32 [B] on the device, or NULL): a padded batch.  Sequence b
+ *    has lengths[b] tokens (taken into [0, L]); rows of y at and behind that
+ *    are left as they were, inputs there are not used, and the final state is
+ *    the one after the last of the lengths[b] tokens (of none: the initial
+ *    state).
+ *  - Outputs must not overlap inputs (SSD_ERR_INVALID_ARG), but for
+ *    final_state, which may be init_state itself: a cache updated in place.
+ *  - No workspace, nothing kept between calls, one launch per call: every call
+ *    can be captured into a CUDA graph.
+ */
+
+/* SSD_CONV_SILU: y = silu(.) instead of the convolution's sum itself. */
+typedef enum { SSD_CONV_SILU = 1 } ssd_conv_flags;
+
+/* batch, seqlen, channels >= 1; width (taps) 2, 3 or 4 (else SSD_ERR_UNSUPPORTED). */
+typedef struct ssd_conv_dims {
+  int64_t batch;    /* B */
+  int64_t seqlen;   /* L (not looked at by ssd_conv_step) */
+  int64_t channels; /* C */
+  int64_t width;    /* W */
+  int32_t io_dtype; /* ssd_dtype of x, y and the states */
+  int32_t flags;    /* ssd_conv_flags */
+} ssd_conv_dims;
+
+/*
+ * Short causal depthwise convolution, what a layer applies to x, B and C before
+ * the scan:
+ *   y[b,t,c] = act(bias[c] + sum_{k<W} weight[c,k] x[b, t-(W-1)+k, c])
+ *   weight [C,W] f32, bias [C] f32 or NULL (= 0),
+ *   init_state [B,W-1,C] io or NULL (= 0): the inputs x[-(W-1)..-1],
+ *   final_state [B,W-1,C] io or NULL: the last W-1 inputs, those of init_state
+ *   among them where the sequence is shorter.
+ */
+ssd_status ssd_conv_fwd(const ssd_conv_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
+                        const float* weight, const float* bias, const void* init_state, const int32_t* lengths,
+                        void* y, int64_t y_bstride, int64_t y_tstride, void* final_state, void* stream);
+
+/*
+ * One token of it: x, y [B,C] (rows x_bstride, y_bstride apart), state
+ * [B,W-1,C] io (the last W-1 inputs on entry; shifted by x on return).
+ */
+ssd_status ssd_conv_step(const ssd_conv_dims* d, const void* x, int64_t x_bstride, const float* weight,
+                         const float* bias, void* state, void* y, int64_t y_bstride, void* stream);
+
+/* SSD_SELECTIVE_SOFTPLUS: the step is softplus(dt + dt_bias) instead of dt + dt_bias. */
+typedef enum { SSD_SELECTIVE_SOFTPLUS = 1 } ssd_selective_flags;
+
+/* batch, seqlen, channels >= 1; 1 <= dstate <= 128 (else SSD_ERR_UNSUPPORTED); ngroups >= 1 dividing channels. */
+typedef struct ssd_selective_dims {
+  int64_t batch;    /* B */
+  int64_t seqlen;   /* L (not looked at by ssd_selective_step) */
+  int64_t channels; /* C */
+  int64_t dstate;   /* N */
+  int64_t ngroups;  /* G: channel c reads group c / (C/G) of Bm and Cm */
+  int32_t io_dtype; /* ssd_dtype of x, dt, Bm, Cm, z and y */
+  int32_t flags;    /* ssd_selective_flags */
+} ssd_selective_dims;
+
+/*
+ * The selective scan with a step of its own for every channel and a decay rate
+ * for every state entry -- the diagonal state matrix of
+ * "告别Transformer的二次方噩梦：用Mamba（S6）模型在长文本任务中实现线性时间推理" §2.1, with
+ * input-dependent dt, B and C; the scans above are its form with a step and a
+ * rate shared by a head's channels:
+ *     s = softplus(dt[b,t,c] + dt_bias[c])          (or dt + dt_bias)
+ *     h_t[n] = exp(s A[c,n]) h_{t-1}[n] + s Bm[b,t,g,n] x[b,t,c]
+ *     y = sum_n Cm[b,t,g,n] h_t[n] + D[c] x[b,t,c],  times silu(z[b,t,c]) where z is given
+ *   x, dt, z, y: rows of C channels (z may be NULL); A [C,N] f32, D, dt_bias
+ *   [C] f32 or NULL (= 0);
+ *   Bm, Cm: rows of G*N entries with one pair of strides for both;
+ *   init_state, final_state [B,C,N] f32 or NULL.
+ */
+ssd_status ssd_selective_fwd(const ssd_selective_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
+                             const void* dt, int64_t dt_bstride, int64_t dt_tstride, const float* A, const void* Bm,
+                             const void* Cm, int64_t bc_bstride, int64_t bc_tstride, const float* D, const void* z,
+                             int64_t z_bstride, int64_t z_tstride, const float* dt_bias, const float* init_state,
+                             const int32_t* lengths, void* y, int64_t y_bstride, int64_t y_tstride,
+                             float* final_state, void* stream);
+
+/*
+ * One token of it: x, dt, z, y [B,C], Bm, Cm [B,G,N] (rows *_bstride apart),
+ * state [B,C,N] f32 updated in place.
+ */
+ssd_status ssd_selective_step(const ssd_selective_dims* d, const void* x, int64_t x_bstride, const void* dt,
+                              int64_t dt_bstride, const float* A, const void* Bm, const void* Cm, int64_t bc_bstride,
+                              const float* D, const void* z, int64_t z_bstride, const float* dt_bias, float* state,
+                              void* y, int64_t y_bstride, void* stream);
+
+/* batch, seqlen, features >= 1; ngroups >= 1 dividing features. */
+typedef struct ssd_norm_dims {
+  int64_t batch;    /* B */
+  int64_t seqlen;   /* L */
+  int64_t features; /* F */
+  int64_t ngroups;  /* G: each of the G runs of F/G features has a norm of its own */
+  int32_t io_dtype; /* ssd_dtype of x, z and out */
+  int32_t flags;    /* 0 */
+} ssd_norm_dims;
+
+/*
+ * The gated norm behind a scan:
+ *   u = x silu(z)  (u = x where z is NULL)
+ *   out = weight u / sqrt(mean over the feature's group of u^2 + eps)
+ *   x, z, out: rows of F features (z may be NULL); weight [F] f32 or NULL (= 1); eps >= 0.
+ * out may be x itself with the same strides.
+ */
+ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
+                             const void* z, int64_t z_bstride, int64_t z_tstride, const float* weight, float eps,
+                             void* out, int64_t out_bstride, int64_t out_tstride, void* stream);
+
+/*
  * Read and clear the device status word that bounded waits inside the
  * kernels set (synchronises `stream`).  Returns SSD_OK or SSD_ERR_TIMEOUT.
  */

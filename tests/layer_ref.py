@@ -1,0 +1,109 @@
+"""Plain 64-bit forms of the layer operators (convolution, selective scan, gated norm) with running bounds on the
+error of an f32 evaluation, element by element: the tolerances of their GPU tests.
+
+u = 2^-24 is half a step of f32.  Documented errors of the device functions used in the bounds: __expf(v) is off by
+at most 2 + 1.173 |v| steps, __fdividef by 2 steps, expf by 1, log1pf by 1, ex2.approx by 2 (a step is 2^-23 of the
+value)."""
+import numpy as np
+
+U = 2.0 ** -24
+STEP = 2.0 ** -23
+HALF = {"f32": U, "bf16": 2.0 ** -8}  # half a step of the stored type, relative to the value
+
+
+def stored(ref, bound, io):
+    """Tolerance of a value of error `bound` once it is rounded to `io`."""
+    return bound + HALF[io] * (np.abs(ref) + bound) + 1e-37
+
+
+def sigmoid(v):
+    return 0.5 * (1.0 + np.tanh(0.5 * v))
+
+
+def silu(v):
+    return v * sigmoid(v)
+
+
+def silu_rel(v):
+    """Relative error of v / (1 + __expf(-v)): the exponential's counts by its share 1 - sigmoid of the sum."""
+    return STEP * ((2 + 1.173 * np.abs(v)) * (1 - sigmoid(v)) + 0.5 + 2 + 0.5)
+
+
+def conv(x, weight, bias, init, lengths, use_silu):
+    """x [B,L,C], weight [C,W], init [B,W-1,C]; returns y, its f32 bound, final state."""
+    B, L, C = x.shape
+    W = weight.shape[1]
+    y, bound = np.zeros((B, L, C)), np.zeros((B, L, C))
+    state = np.zeros((B, W - 1, C))
+    for b in range(B):
+        n = L if lengths is None else min(max(int(lengths[b]), 0), L)
+        seen = np.concatenate([init[b], x[b, :n]])
+        v = np.tile(bias, (n, 1))
+        mag = np.abs(v)
+        for k in range(W):
+            v = v + seen[k:k + n] * weight[:, k]
+            mag = mag + np.abs(seen[k:k + n] * weight[:, k])
+        e = (W + 1) * U * mag  # W fused steps, each rounding a partial sum of at most `mag`
+        if use_silu:
+            # |silu'| <= 1.1
+            y[b, :n] = silu(v)
+            bound[b, :n] = 1.1 * e + (np.abs(silu(v)) + 1.1 * e) * silu_rel(v)
+        else:
+            y[b, :n], bound[b, :n] = v, e
+        state[b] = seen[n:]
+    return y, bound, state
+
+
+def selective(x, dt, A, Bm, Cm, D, z, dt_bias, init, lengths, softplus, rate_steps=2.0):
+    """x, dt, z [B,L,C]; A [C,N]; Bm, Cm [B,L,G,N]; init [B,C,N].  Returns y, its f32 bound, final state, its bound.
+    rate_steps: steps by which the kernel's 2^v may be off."""
+    B, L, C = x.shape
+    N, G = A.shape[1], Bm.shape[2]
+    ends = np.full(B, L) if lengths is None else np.clip(np.asarray(lengths, dtype=np.int64), 0, L)
+    h, mag, err = init.copy(), np.abs(init), np.zeros_like(init)
+    y, yb = np.zeros((B, L, C)), np.zeros((B, L, C))
+    group = np.arange(C) // (C // G)
+    for t in range(L):
+        live = (t < ends)[:, None, None]
+        v = dt[:, t] + dt_bias
+        s = np.logaddexp(v, 0.0) if softplus else v
+        # v is rounded once; softplus' = sigmoid <= s where s is small and <= 1, so v's rounding is u |v| of s at
+        # most for v < 0 and u |v| <= u s for v >= 0; expf, log1pf and the sum: 4 steps
+        ds = U * np.abs(v) + (4 * STEP if softplus else 0.0)
+        ds = np.where(softplus, ds, U)
+        sa = s[:, :, None] * A
+        a = np.exp(sa)
+        # the exponent: s's error, the rounding of A log2(e) (twice: constant and product) and of the product
+        da = np.abs(sa) * (ds[:, :, None] + 4 * U) + rate_steps * STEP
+        bt, ct = Bm[:, t][:, group], Cm[:, t][:, group]
+        inp = (s * x[:, t])[:, :, None] * bt
+        di = np.abs(inp) * (ds[:, :, None] + 3 * U)
+        h2 = a * h + inp
+        mag2 = a * mag + np.abs(inp)
+        err2 = a * (1 + da) * err + a * mag * da + di + U * mag2
+        h, mag, err = (np.where(live, p, q) for p, q in ((h2, h), (mag2, mag), (err2, err)))
+        out = np.sum(ct * h, -1) + D * x[:, t]
+        whole = np.sum(np.abs(ct) * mag, -1) + np.abs(D * x[:, t])
+        e = np.sum(np.abs(ct) * err, -1) + (N + 2) * U * whole
+        if z is not None:
+            g = silu(z[:, t])
+            e = np.abs(g) * (e + (np.abs(out) + e) * (silu_rel(z[:, t]) + U))
+            out = out * g
+        y[:, t], yb[:, t] = np.where(live[:, :, 0], out, 0.0), np.where(live[:, :, 0], e, 0.0)
+    return y, yb, h, err + 4 * U * mag
+
+
+def gated_norm(x, z, weight, eps, ngroups):
+    """x, z [..., F]; returns out and its f32 bound."""
+    F = x.shape[-1]
+    u, rel = (x, np.zeros_like(x)) if z is None else (x * silu(z), silu_rel(z) + U)
+    v = u.reshape(x.shape[:-1] + (ngroups, F // ngroups))
+    ms = np.mean(v * v, -1, keepdims=True)
+    out = (v / np.sqrt(ms + eps)).reshape(x.shape) * weight
+    # sum of squares: each term off by twice its factor's error (weighted by its square) and by the roundings along
+    # its path: the elements of one thread of 512 (of 32 or fewer where the run is short: at most 32), 5 shuffles, 32 warps; then mean, eps, root and reciprocal
+    path = F // ngroups // 512 + 32 + 5 + 32
+    r = rel.reshape(v.shape)
+    dm = np.sum(v * v * 2 * r, -1, keepdims=True) / np.maximum(np.sum(v * v, -1, keepdims=True), 1e-300) + path * U
+    dm = np.broadcast_to(dm, v.shape).reshape(x.shape)
+    return out, np.abs(out) * (rel + 0.5 * dm + 8 * U)
