@@ -45,21 +45,30 @@ struct Taps {
   // old[0] is the oldest of the W-1 inputs before `in`
   template <typename T>
   __device__ __forceinline__ Pack<T, VEC> apply(const float (&old)[W - 1][VEC], const float (&in)[VEC]) const {
-    Pack<T, VEC> out;
+    float out[VEC];
+    if constexpr (VEC == 1) {
+      float acc = b[0];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float acc = b[i];
+      for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][0], old[k][0], acc);
+      acc = fmaf(w[W - 1][0], in[0], acc);
+      out[0] = SILU ? silu(acc) : acc;
+    } else {
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], old[k][i], acc);
-      acc = fmaf(w[W - 1][i], in[i], acc);
-      out.v[i] = from_f32<T>(SILU ? silu(acc) : acc);
+      for (int i = 0; i < VEC; i += 2) {
+        F2 acc{b[i], b[i + 1]};
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) acc = fma2(F2{w[k][i], w[k][i + 1]}, F2{old[k][i], old[k][i + 1]}, acc);
+        acc = fma2(F2{w[W - 1][i], w[W - 1][i + 1]}, F2{in[i], in[i + 1]}, acc);
+        if (SILU) acc = silu2(acc);
+        out[i] = acc.x, out[i + 1] = acc.y;
+      }
     }
-    return out;
+    return to_pack<T, VEC>(out);
   }
 };
 
 template <typename T, int W, int VEC, bool SILU>
-__global__ void __launch_bounds__(THREADS) k_conv_fwd(const Args<T> a) {
+__global__ void __launch_bounds__(THREADS, 4) k_conv_fwd(const Args<T> a) {
   const uint32_t idx = blockIdx.x * THREADS + threadIdx.x;
   if (idx >= a.total) return;
   const uint32_t r = idx / a.nvec;
@@ -73,17 +82,14 @@ __global__ void __launch_bounds__(THREADS) k_conv_fwd(const Args<T> a) {
   float old[W - 1][VEC];  // the W-1 inputs before the next token, oldest first
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
-    Pack<T, VEC> v;
+    Pack<T, VEC> v{};
     if (tile != 0) {
       v = load_pack<T, VEC>(a.x.row(b, t0 - (W - 1) + k) + c);
     } else if (a.init) {
       v = load_pack<T, VEC>(a.init + (b * (W - 1) + k) * a.C + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v.v[i] = from_f32<T>(0.f);
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) old[k][i] = to_f32(v.v[i]);
+    for (int i = 0; i < VEC; ++i) old[k][i] = v.get(i);
   }
   if (tile == 0 && a.final_state) {
     // The thread that read these channels of init_state writes their final
@@ -92,43 +98,43 @@ __global__ void __launch_bounds__(THREADS) k_conv_fwd(const Args<T> a) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       const int64_t t = len - (W - 1) + k;
-      if (t >= 0) {
+      last[k] = Pack<T, VEC>{};
+      if (t >= 0)
         last[k] = load_pack<T, VEC>(a.x.row(b, t) + c);
-      } else {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-          if (j == (int)(t + W - 1)) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) last[k].v[i] = from_f32<T>(old[j][i]);
-          }
-      }
+      else if (a.init)
+        last[k] = load_pack<T, VEC>(a.init + (b * (W - 1) + (t + W - 1)) * a.C + c);
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) store_pack<T, VEC>(a.final_state + (b * (W - 1) + k) * a.C + c, last[k]);
   }
   Taps<W, VEC, SILU> taps;
   taps.load(a.weight, a.bias, c);
-  for (int64_t t = t0; t < t1; t += AHEAD) {
+  const T* x = a.x.row(b, t0) + c;
+  T* y = a.y.row(b, t0) + c;
+  auto token = [&](const Pack<T, VEC>& in) {
+    float cur[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) cur[i] = in.get(i);
+    store_pack<T, VEC>(y, taps.template apply<T>(old, cur));
+    y += a.y.ts;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+      for (int k = 0; k + 1 < W - 1; ++k) old[k][i] = old[k + 1][i];
+      old[W - 2][i] = cur[i];
+    }
+  };
+  int64_t t = t0;
+#pragma unroll 1
+  for (; t + AHEAD <= t1; t += AHEAD) {
     Pack<T, VEC> in[AHEAD];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (t + j < t1) in[j] = load_pack<T, VEC>(a.x.row(b, t + j) + c);
+    for (int j = 0; j < AHEAD; ++j, x += a.x.ts) in[j] = load_pack<T, VEC>(x);
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      if (t + j < t1) {
-        float cur[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) cur[i] = to_f32(in[j].v[i]);
-        store_pack<T, VEC>(a.y.row(b, t + j) + c, taps.template apply<T>(old, cur));
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-          for (int k = 0; k + 1 < W - 1; ++k) old[k][i] = old[k + 1][i];
-          old[W - 2][i] = cur[i];
-        }
-      }
-    }
+    for (int j = 0; j < AHEAD; ++j) token(in[j]);
   }
+#pragma unroll 1
+  for (; t < t1; ++t, x += a.x.ts) token(load_pack<T, VEC>(x));
 }
 
 template <typename T, int W, int VEC, bool SILU>
@@ -150,8 +156,8 @@ __global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, 
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) old[k][i] = to_f32(seen[k].v[i]);
-    cur[i] = to_f32(seen[W - 1].v[i]);
+    for (int k = 0; k < W - 1; ++k) old[k][i] = seen[k].get(i);
+    cur[i] = seen[W - 1].get(i);
   }
   store_pack<T, VEC>(y + b * ybs + c, taps.template apply<T>(old, cur));
 #pragma unroll

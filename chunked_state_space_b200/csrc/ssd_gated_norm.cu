@@ -26,7 +26,7 @@ struct Args {
 template <typename T, int VEC>
 __device__ __forceinline__ void gated(const Pack<T, VEC>& x, const Pack<T, VEC>& z, bool gate, float (&u)[VEC]) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) u[i] = gate ? to_f32(x.v[i]) * silu(to_f32(z.v[i])) : to_f32(x.v[i]);
+  for (int i = 0; i < VEC; ++i) u[i] = gate ? x.get(i) * silu(z.get(i)) : x.get(i);
 }
 
 // One run per warp (BLOCK false, four warps of a block on four runs) or per block.
@@ -81,13 +81,13 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
       if (p < pieces) {
         // a run longer than the registers hold is read again
         if (pieces > (int64_t)PER * all) gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u[k]);
-        Pack<T, VEC> o;
+        float o[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float w = a.weight ? a.weight[g * a.n + p * VEC + i] : 1.f;
-          o.v[i] = from_f32<T>(u[k][i] * inv * w);
+          o[i] = u[k][i] * inv * w;
         }
-        store_pack<T, VEC>(out + p * VEC, o);
+        store_pack<T, VEC>(out + p * VEC, to_pack<T, VEC>(o));
       }
     }
   }

@@ -15,11 +15,47 @@ struct Rows {
   __device__ __forceinline__ T* row(int64_t b, int64_t t) const { return p + b * bs + t * ts; }
 };
 
-// VEC consecutive elements moved by one access (16 bytes, or one element where
-// the rows do not start on 16 bytes).
+// VEC consecutive elements as one access moves them: 16 bytes (8: four f32's
+// worth of bf16), or one element where rows do not start on 16 bytes.  Kept as
+// whole words until an element is asked for: unpacked where they are loaded,
+// each load would be waited for on the spot.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T v[VEC];
+struct Pack;
+template <>
+struct alignas(16) Pack<__nv_bfloat16, 8> {
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void set2(int i, float lo, float hi) {  // elements i (even) and i + 1
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    w[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <>
+struct alignas(8) Pack<__nv_bfloat16, 4> {
+  uint32_t w[2];
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+template <>
+struct alignas(16) Pack<float, 4> {
+  float w[4];
+  __device__ __forceinline__ float get(int i) const { return w[i]; }
+  __device__ __forceinline__ void set2(int i, float lo, float hi) { w[i] = lo, w[i + 1] = hi; }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+  uint16_t w;
+  __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)w << 16); }
+  __device__ __forceinline__ void set(float v) { w = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+template <>
+struct Pack<float, 1> {
+  float w;
+  __device__ __forceinline__ float get(int) const { return w; }
+  __device__ __forceinline__ void set(float v) { w = v; }
 };
 
 template <typename T, int VEC>
@@ -30,9 +66,78 @@ template <typename T, int VEC>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v) {
   *reinterpret_cast<Pack<T, VEC>*>(p) = v;
 }
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> to_pack(const float (&v)[VEC]) {
+  Pack<T, VEC> r;
+  if constexpr (VEC == 1) {
+    r.set(v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) r.set2(i, v[i], v[i + 1]);
+  }
+  return r;
+}
+
+// Two f32 values per instruction (packed f32x2), each rounded like the scalar
+// operation.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 both(float v) { return {v, v}; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+constexpr float LOG2E = 1.4426950408889634f;
 
 // v / (1 + e^-v); e^-v = inf for v < -88 gives -0, as the limit does.
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.0f + ex2(v * -LOG2E)); }
+__device__ __forceinline__ F2 silu2(F2 v) {
+  const F2 t = mul2(v, both(-LOG2E)), d = add2(F2{ex2(t.x), ex2(t.y)}, both(1.0f));
+  return mul2(v, F2{rcp(d.x), rcp(d.y)});
+}
 
 __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t L) {
   if (!lengths) return L;

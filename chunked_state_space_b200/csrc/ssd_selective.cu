@@ -13,17 +13,15 @@
 // registers over the whole sequence; a block takes 128 / LPC channels of one
 // group.  Its inputs come tile by tile: the next tile's rows are loaded into
 // registers while this one is computed; step and scaled input are formed once
-// per (token, channel) and put in shared memory twice each, as the operands of
-// packed f32x2 instructions; B and C are widened to f32 once per tile.  The LPC
-// partial sums of y of LPC tokens are reduced together, each exchange halving
-// what a lane still holds, so that lane q ends up with token q's sum.
+// per (token, channel) and put in shared memory; B and C are widened to f32 once per tile.
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace selective {
 
-constexpr int THREADS = 128;
-constexpr float LOG2E = 1.4426950408889634f;
+// of a block: lanes of the recurrence, and two teams of helpers (operands in, outputs out)
+constexpr int LANES = 128, HELPERS = 64, THREADS = LANES + 2 * HELPERS;
+constexpr int64_t SCHEDULERS = 4 * 148;  // warp schedulers of the GPU
 
 template <typename T>
 struct Args {
@@ -36,252 +34,397 @@ struct Args {
   int64_t L;
   int C, N, G, per_group;
   uint32_t blocks_per_group, total;
-  bool softplus, vec;
+  bool softplus, vec, bvec;
 };
-
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// Two f32 lanes per instruction, each rounded like the scalar operation.
-struct F2 {
-  float x, y;
-};
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  const float2 r = vdecay::mul2(make_float2(a.x, a.y), make_float2(b.x, b.y));
-  return {r.x, r.y};
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  const float2 r = vdecay::fma2(make_float2(a.x, a.y), make_float2(b.x, b.y), make_float2(c.x, c.y));
-  return {r.x, r.y};
-}
 
 // max(v, 0) + log1p(e^-|v|).  The exponent's rounding is put back to first
 // order, so that small steps keep f32 accuracy; log1p(e) = e P(e) with P the
 // minimax polynomial of degree 8 of log1p(e) / e on [0, 1] (Remez exchange,
 // P(0) = 1; at most 1.8e-7 off, relative, evaluated in f32).
-__device__ __forceinline__ float softplus(float v) {
-  const float m = -fabsf(v), t = m * LOG2E;
-  const float p = ex2(t), e = fmaf(p, fmaf(m, LOG2E, -t) * 0.69314718f, p);
-  float q = 0.0053648264f;
-  q = fmaf(q, e, -0.030065801f);
-  q = fmaf(q, e, 0.07920455f);
-  q = fmaf(q, e, -0.13753803f);
-  q = fmaf(q, e, 0.19153656f);
-  q = fmaf(q, e, -0.24857163f);
-  q = fmaf(q, e, 0.33321324f);
-  q = fmaf(q, e, -0.49999648f);
-  q = fmaf(q, e, 1.0f);
-  return fmaf(q, e, v < 0.f ? 0.f : v);  // v, not max(v, 0): NaN stays
+__device__ __forceinline__ F2 softplus2(F2 v) {
+  const F2 m{-fabsf(v.x), -fabsf(v.y)}, t = mul2(m, both(LOG2E));
+  const F2 p{ex2(t.x), ex2(t.y)};
+  const F2 lost = mul2(fma2(m, both(LOG2E), F2{-t.x, -t.y}), both(0.69314718f));
+  const F2 e = fma2(p, lost, p);
+  F2 q = both(0.0053648264f);
+  q = fma2(q, e, both(-0.030065801f));
+  q = fma2(q, e, both(0.07920455f));
+  q = fma2(q, e, both(-0.13753803f));
+  q = fma2(q, e, both(0.19153656f));
+  q = fma2(q, e, both(-0.24857163f));
+  q = fma2(q, e, both(0.33321324f));
+  q = fma2(q, e, both(-0.49999648f));
+  q = fma2(q, e, both(1.0f));
+  return fma2(q, e, F2{v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y});  // v, not max(v, 0): NaN stays
 }
+__device__ __forceinline__ float softplus(float v) { return softplus2(both(v)).x; }
 
-template <typename T, int NS, int LPC, bool VEC>
+template <typename T, int NS, int LPC, bool VEC, bool BVEC>
 struct Shape {
-  static constexpr int CB = THREADS / LPC;                 // channels of a block
+  static constexpr int CB = LANES / LPC;                       // channels of a block
   static constexpr int NP = NS * LPC;                      // state entries, the last ones empty where N is less
-  static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;  // elements per load
-  // tokens of a tile: E elements of x per thread, fewer where B and C would not leave room
-  static constexpr int E = NP <= 32 ? 8 : NP == 64 ? 4 : 2;
-  static constexpr int TT = LPC == 1 ? 16 : E * LPC;
-  static constexpr int NX = (TT * CB / V + THREADS - 1) / THREADS;  // loads of x (dt, z) per thread
-  static constexpr int NB = (TT * NP / V + THREADS - 1) / THREADS;  // loads of B (C) per thread
-  // a row of y sums: lanes of a warp hold 32 / LPC channels of LPC tokens, which should fall on different banks
-  static constexpr int YS = LPC == 1 ? CB : LPC == 2 ? CB + 16 : LPC == 4 ? CB + 8 : CB + 4;
-  static_assert(TT % LPC == 0, "a tile is a whole number of reductions");
-  static_assert(NP % V == 0 && CB % V == 0, "rows of a tile are whole pieces");
-  // Where (token, channel) lies in a tile of 16-byte entries: a thread writes V neighbouring channels, one per
-  // instruction, so they are turned by the piece's number to fall on different banks; the channels that a warp reads
-  // together share the turn.
+  static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;   // elements per load of x, dt, z and per store of y
+  static constexpr int VB = BVEC ? 16 / (int)sizeof(T) : 1;  // ... per load of B, C
+  // tokens of a tile: eight elements of x per helper thread, fewer where B and C would not leave room (in shared
+  // memory, or in registers as single elements)
+  static constexpr int TT = NP <= 16 ? 8 * HELPERS / CB : NP == 32 ? (BVEC ? 32 : 16) : NP == 64 ? (BVEC ? 16 : 8) : 8;
+  static constexpr int XP = TT * CB / V, BP = TT * NP / VB;        // pieces of a tile of x (dt, z), of B (C)
+  static constexpr int NX = (XP + HELPERS - 1) / HELPERS;          // of them, per helper thread
+  static constexpr int NB = (2 * BP + HELPERS - 1) / HELPERS;      // (of B and C together)
+  // y's sums over the states are left in PW parts per (token, channel), which the output pass adds up; more lanes than
+  // that exchange theirs first, RED tokens together, each exchange halving what a lane still holds.
+  static constexpr int PW = LPC < 4 ? LPC : 4, RED = LPC / PW;
+  static constexpr int U = RED < 2 ? 2 : RED;  // tokens that a lane works on together
+  static constexpr int ROWS = TT + 2 * U;      // rows of operands: a tile, and what the loop reads behind it for nothing
+  static_assert(TT % (2 * U) == 0, "a tile is a whole number of turns of its loop");
+  static_assert(NP % VB == 0 && CB % V == 0, "rows of a tile are whole pieces");
+  // Where (token, channel) lies in a tile of 8-byte entries: a thread writes V neighbouring channels, two per
+  // instruction, so its pairs are turned by the piece's number to fall on different banks; the channels that a warp
+  // reads together share the turn or lie in different pieces.
   __device__ static __forceinline__ int at(int t, int ch) {
-    if (V == 8) return t * CB + (ch ^ ((t * (CB / 8) + (ch >> 3)) & 7));
-    if (V == 4) return t * CB + (ch ^ (((t * (CB / 4) + (ch >> 2)) >> 1) & 3));
-    return t * CB + ch;
+    const int i = t * (CB / V) + ch / V;
+    const int turn = V == 8 ? (i >> 1) & 3 : V == 4 ? (i >> 2) & 1 : 0;
+    return t * CB + (ch ^ (turn << 1));
+  }
+  // The same for entries of PW f32 (up to 16 bytes), which a thread reads one per instruction.
+  __device__ static __forceinline__ int sum_at(int t, int ch) {
+    const int i = t * (CB / V) + ch / V;
+    return (t * CB + (ch ^ (V == 8 ? i & 7 : V == 4 ? (i >> 1) & 3 : 0))) * PW;
   }
 };
 
-template <typename T, int NS, int LPC, bool VEC>
-__global__ void __launch_bounds__(THREADS) k_selective(const Args<T> a) {
-  using S = Shape<T, NS, LPC, VEC>;
-  constexpr int CB = S::CB, NP = S::NP, V = S::V, TT = S::TT, NX = S::NX, NB = S::NB, YS = S::YS;
-  __shared__ float4 s_step[TT * CB];  // (s, s, s x, s x)
-  __shared__ __align__(16) float s_b[TT * NP], s_c[TT * NP];
-  __shared__ __align__(16) float s_y[TT * YS];
-  __shared__ float s_D[CB], s_bias[CB];
+// The block's barriers beside __syncthreads(): FULL + k, the operands of
+// buffer k are written and its sums have been taken; DONE + k, its operands
+// have been used and its sums are written.  Every thread of the block takes
+// part in each of them once per tile, waiting or only arriving.
+enum { FULL = 1, DONE = 3 };
+__device__ __forceinline__ void wait_for(int bar) { asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(THREADS) : "memory"); }
+__device__ __forceinline__ void arrive_at(int bar) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(bar), "n"(THREADS) : "memory");
+}
+
+template <typename T, int NS, int LPC, bool VEC, bool BVEC>
+__global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective(const Args<T> a) {
+  using S = Shape<T, NS, LPC, VEC, BVEC>;
+  constexpr int CB = S::CB, NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
+                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS;
+  __shared__ __align__(16) float2 s_step[2][ROWS * CB];    // (s, s x)
+  __shared__ __align__(16) float s_bc[2][2][ROWS * NP];    // B, C
+  __shared__ __align__(16) float s_y[2][TT * CB * PW];
+  __shared__ __align__(16) float s_D[CB], s_bias[CB];
   const uint32_t r = blockIdx.x / a.blocks_per_group, cb = blockIdx.x - r * a.blocks_per_group;
   const uint32_t b = r / a.G, g = r - b * a.G;
   const int c0 = (int)g * a.per_group + (int)cb * CB;  // first channel of the block
   const int nc = min(CB, ((int)g + 1) * a.per_group - c0);
-  const int tid = threadIdx.x, q = tid % LPC, ch = tid / LPC;
+  const int tid = threadIdx.x;
   const int64_t len = row_length(a.lengths, b, a.L);
-  const int64_t at = ((int64_t)b * a.C + c0 + ch) * a.N;
+  const int64_t tiles = (len + TT - 1) / TT;
+  for (int i = tid; i < CB; i += THREADS) {
+    s_D[i] = a.D && i < nc ? a.D[c0 + i] : 0.f;
+    s_bias[i] = a.dt_bias && i < nc ? a.dt_bias[c0 + i] : 0.f;
+  }
+  __syncthreads();
+
+  if (tid >= LANES + HELPERS) {
+    // ---- output: add up the sums, skip and gate, store
+    const int me = tid - LANES - HELPERS;
+    const bool gate = a.z.p != nullptr;
+    for (int k = 0; k < 2 && k < tiles; ++k) arrive_at(FULL + k);
+    Pack<T, V> nx[NX], nz[NX];
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+      for (int k = 0; k < NX; ++k) {
+        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
+        if (i < XP && t0 + t < len && c < nc) {
+          nx[k] = load_pack<T, V>(a.x.row(b, t0 + t) + c0 + c);
+          if (gate) nz[k] = load_pack<T, V>(a.z.row(b, t0 + t) + c0 + c);
+        }
+      }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int64_t tile = 0; tile < tiles; ++tile) {
+      const int64_t t0 = tile * TT;
+      const int k2 = (int)(tile & 1);
+      Pack<T, V> x[NX], z[NX];
+#pragma unroll
+      for (int k = 0; k < NX; ++k) x[k] = nx[k], z[k] = nz[k];
+      if (tile + 1 < tiles) fetch(t0 + TT);
+      wait_for(DONE + k2);
+      auto sum = [&](int t, int c) {
+        const float* p = &s_y[k2][S::sum_at(t, c)];
+        if constexpr (PW == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(p);
+          return (v.x + v.y) + (v.z + v.w);
+        } else if constexpr (PW == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(p);
+          return v.x + v.y;
+        } else {
+          return p[0];
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < NX; ++k) {
+        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
+        if (i < XP && t0 + t < len && c < nc) {
+          float out[V];
+          if constexpr (V == 1) {
+            out[0] = fmaf(s_D[c], x[k].get(0), sum(t, c));
+            if (gate) out[0] *= silu(z[k].get(0));
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              F2 y = fma2(F2{s_D[c + e], s_D[c + e + 1]}, F2{x[k].get(e), x[k].get(e + 1)},
+                          F2{sum(t, c + e), sum(t, c + e + 1)});
+              if (gate) y = mul2(y, silu2(F2{z[k].get(e), z[k].get(e + 1)}));
+              out[e] = y.x, out[e + 1] = y.y;
+            }
+          }
+          store_pack<T, V>(a.y.row(b, t0 + t) + c0 + c, to_pack<T, V>(out));
+        }
+      }
+      if (tile + 2 < tiles) arrive_at(FULL + k2);
+    }
+    return;
+  }
+
+  if (tid >= LANES) {
+    // ---- operands: the step and the scaled input of every (token, channel), B and C
+    const int me = tid - LANES;
+    Pack<T, V> nx[NX], nd[NX];
+    Pack<T, VB> nb[NB];
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+      for (int k = 0; k < NX; ++k) {
+        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
+        if (i < XP && t0 + t < len && c < nc) {
+          nx[k] = load_pack<T, V>(a.x.row(b, t0 + t) + c0 + c);
+          nd[k] = load_pack<T, V>(a.dt.row(b, t0 + t) + c0 + c);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int ii = me + k * HELPERS, i = ii < BP ? ii : ii - BP, t = i / (NP / VB), n = i % (NP / VB) * VB;
+        if (ii < 2 * BP && t0 + t < len && n < a.N)
+          nb[k] = load_pack<T, VB>((ii < BP ? a.bm : a.cm).row(b, t0 + t) + (int64_t)g * a.N + n);
+      }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int64_t tile = 0; tile < tiles; ++tile) {
+      const int64_t t0 = tile * TT;
+      const int k2 = (int)(tile & 1);
+      if (tile >= 2) wait_for(DONE + k2);
+      // behind the sequence's end the step is 0, which leaves the state as it is
+#pragma unroll
+      for (int k = 0; k < NX; ++k) {
+        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
+        if (i < XP) {
+          const bool in = t0 + t < len && c < nc;
+          if constexpr (V == 1) {
+            float s = 0.f, sx = 0.f;
+            if (in) {
+              s = nd[k].get(0) + s_bias[c];
+              if (a.softplus) s = softplus(s);
+              sx = s * nx[k].get(0);
+            }
+            s_step[k2][S::at(t, c)] = make_float2(s, sx);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              F2 s = both(0.f), sx = both(0.f);
+              if (in) {
+                s = add2(F2{nd[k].get(e), nd[k].get(e + 1)}, F2{s_bias[c + e], s_bias[c + e + 1]});
+                if (a.softplus) s = softplus2(s);
+                sx = mul2(s, F2{nx[k].get(e), nx[k].get(e + 1)});
+              }
+              *reinterpret_cast<float4*>(&s_step[k2][S::at(t, c + e)]) = make_float4(s.x, sx.x, s.y, sx.y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int ii = me + k * HELPERS, i = ii < BP ? ii : ii - BP, t = i / (NP / VB), n = i % (NP / VB) * VB;
+        if (ii < 2 * BP) {
+          const bool in = t0 + t < len && n < a.N;
+          float* to = &s_bc[k2][ii < BP ? 0 : 1][i * VB];
+#pragma unroll
+          for (int e = 0; e < VB; ++e) to[e] = in ? nb[k].get(e) : 0.f;
+        }
+      }
+      arrive_at(FULL + k2);
+      if (tile + 1 < tiles) fetch(t0 + TT);
+    }
+    for (int64_t tile = tiles > 2 ? tiles - 2 : 0; tile < tiles; ++tile) arrive_at(DONE + (int)(tile & 1));
+    return;
+  }
+
+  // ---- the recurrence
+  const int q = tid % LPC, ch = tid / LPC;
   float A2[NS], h[NS];
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const int n = q * NS + k;
     const bool in = ch < nc && n < a.N;
     A2[k] = in ? a.A[(int64_t)(c0 + ch) * a.N + n] * LOG2E : 0.f;
-    h[k] = in && a.init ? a.init[at + n] : 0.f;
+    h[k] = in && a.init ? a.init[((int64_t)b * a.C + c0 + ch) * a.N + n] : 0.f;
   }
-  if (tid < CB) {
-    s_D[tid] = a.D && tid < nc ? a.D[c0 + tid] : 0.f;
-    s_bias[tid] = a.dt_bias && tid < nc ? a.dt_bias[c0 + tid] : 0.f;
-  }
-  const bool gate = a.z.p != nullptr;
-  Pack<T, V> nx[NX], nd[NX], nz[NX], nb[NB], ncm[NB];  // the next tile's rows
-  auto fetch = [&](int64_t t0) {
+  struct Operands {  // of U tokens
+    float2 st[U];
+    float b[U][NS], c[U][NS];
+  };
+  auto read = [&](int k2, int tg, Operands& o) {
 #pragma unroll
-    for (int k = 0; k < NX; ++k) {
-      const int i = tid + k * THREADS, t = i / (CB / V), c = i % (CB / V) * V;
-      if (i < TT * CB / V && t0 + t < len && c < nc) {
-        nx[k] = load_pack<T, V>(a.x.row(b, t0 + t) + c0 + c);
-        nd[k] = load_pack<T, V>(a.dt.row(b, t0 + t) + c0 + c);
-        if (gate) nz[k] = load_pack<T, V>(a.z.row(b, t0 + t) + c0 + c);
-      }
-    }
+    for (int j = 0; j < U; ++j) {
+      const int t = tg + j;
+      o.st[j] = s_step[k2][S::at(t, ch)];
+      const float* bt = &s_bc[k2][0][t * NP + q * NS];
+      const float* ct = &s_bc[k2][1][t * NP + q * NS];
+      if constexpr (NS % 4 == 0) {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int i = tid + k * THREADS, t = i / (NP / V), n = i % (NP / V) * V;
-      if (i < TT * NP / V && t0 + t < len && n < a.N) {
-        nb[k] = load_pack<T, V>(a.bm.row(b, t0 + t) + (int64_t)g * a.N + n);
-        ncm[k] = load_pack<T, V>(a.cm.row(b, t0 + t) + (int64_t)g * a.N + n);
+        for (int k = 0; k < NS; k += 4) {
+          *reinterpret_cast<float4*>(&o.b[j][k]) = *reinterpret_cast<const float4*>(bt + k);
+          *reinterpret_cast<float4*>(&o.c[j][k]) = *reinterpret_cast<const float4*>(ct + k);
+        }
+      } else if constexpr (NS == 2) {
+        *reinterpret_cast<float2*>(o.b[j]) = *reinterpret_cast<const float2*>(bt);
+        *reinterpret_cast<float2*>(o.c[j]) = *reinterpret_cast<const float2*>(ct);
+      } else {
+        o.b[j][0] = bt[0], o.c[j][0] = ct[0];
       }
     }
   };
-  fetch(0);
-  __syncthreads();  // s_D, s_bias
-  for (int64_t t0 = 0; t0 < len; t0 += TT) {
-    // stage this tile; behind the sequence's end the step is 0, which leaves the state as it is
-    Pack<T, V> x[NX], z[NX];
+  auto rates = [&](const Operands& o, float (&e)[U][NS]) {
 #pragma unroll
-    for (int k = 0; k < NX; ++k) {
-      x[k] = nx[k];
-      z[k] = nz[k];
-      const int i = tid + k * THREADS, t = i / (CB / V), c = i % (CB / V) * V;
-      if (i < TT * CB / V) {
-        const bool in = t0 + t < len && c < nc;
+    for (int j = 0; j < U; ++j) {
+      if constexpr (NS == 1) {
+        e[j][0] = ex2(o.st[j].x * A2[0]);
+      } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float s = 0.f, sx = 0.f;
-          if (in) {
-            s = to_f32(nd[k].v[e]) + s_bias[c + e];
-            if (a.softplus) s = softplus(s);
-            sx = s * to_f32(x[k].v[e]);
-          }
-          s_step[S::at(t, c + e)] = make_float4(s, s, sx, sx);
+        for (int k = 0; k < NS; k += 2) {
+          const F2 v = mul2(both(o.st[j].x), F2{A2[k], A2[k + 1]});
+          e[j][k] = ex2(v.x);
+          e[j][k + 1] = ex2(v.y);
         }
       }
     }
+  };
+  // Where a group's sums take two exchanges they are stored with the next group's: by then the last has come back.
+  constexpr bool DEFER = RED > 2;
+  float mine[U / RED], last = 0.f;
+  auto store = [&](int k2, int tg) {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int i = tid + k * THREADS, t = i / (NP / V), n = i % (NP / V) * V;
-      if (i < TT * NP / V) {
-        const bool in = t0 + t < len && n < a.N;
+    for (int j = 0; j < U / RED; ++j) s_y[k2][S::sum_at(tg + j + q / PW, ch) + q % PW] = DEFER ? mine[j] + last : mine[j];
+  };
+  auto finish = [&](int k2, int tg, const Operands& o, const float (&e)[U][NS]) {
+    float part[U];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          s_b[i * V + e] = in ? to_f32(nb[k].v[e]) : 0.f;
-          s_c[i * V + e] = in ? to_f32(ncm[k].v[e]) : 0.f;
+    for (int j = 0; j < U; ++j) {
+      if constexpr (NS == 1) {
+        h[0] = fmaf(e[j][0], h[0], o.st[j].y * o.b[j][0]);
+        part[j] = o.c[j][0] * h[0];
+      } else {
+        F2 y{0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NS; k += 2) {
+          const F2 bx = mul2(both(o.st[j].y), F2{o.b[j][k], o.b[j][k + 1]});
+          const F2 hn = fma2(F2{e[j][k], e[j][k + 1]}, F2{h[k], h[k + 1]}, bx);
+          h[k] = hn.x;
+          h[k + 1] = hn.y;
+          const F2 cv{o.c[j][k], o.c[j][k + 1]};
+          y = k == 0 ? mul2(cv, hn) : fma2(cv, hn, y);
         }
+        part[j] = y.x + y.y;
       }
     }
-    __syncthreads();
-    if (t0 + TT < len) fetch(t0 + TT);
+    if (DEFER && tg > 0) store(k2, tg - U);
+#pragma unroll
+    for (int half = RED / 2; half > 0; half /= 2) {
+      const bool up = (q & (half * PW)) != 0;
+#pragma unroll
+      for (int j = 0; j < half; ++j) {
+        const float give = up ? part[j] : part[j + half], keep = up ? part[j + half] : part[j];
+        const float got = __shfl_xor_sync(0xffffffffu, give, half * PW);
+        if (DEFER && half == 1)
+          part[0] = keep, last = got;
+        else
+          part[j] = keep + got;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < U / RED; ++j) mine[j] = part[j];
+    if (!DEFER) store(k2, tg);
+  };
 #pragma unroll 1
-    for (int tg = 0; tg < TT; tg += LPC) {
-      float part[LPC];
+  for (int64_t tile = 0; tile < tiles; ++tile) {
+    const int k2 = (int)(tile & 1);
+    wait_for(FULL + k2);
+    // Software pipeline over groups of U tokens: while group g is finished, the exponentials of g + 1 are under way
+    // and the operands of g + 2 are loaded.
+    Operands o[2];
+    float e[2][U][NS];
+    read(k2, 0, o[0]);
+    read(k2, U, o[1]);
+    rates(o[0], e[0]);
+#pragma unroll 1
+    for (int tg = 0; tg < TT; tg += 2 * U) {
 #pragma unroll
-      for (int j = 0; j < LPC; ++j) {
-        const int t = tg + j;
-        const float4 st = s_step[S::at(t, ch)];
-        const float* bt = &s_b[t * NP + q * NS];
-        const float* ct = &s_c[t * NP + q * NS];
-        float bv[NS], cv[NS];
-        if constexpr (NS % 4 == 0) {
-#pragma unroll
-          for (int k = 0; k < NS; k += 4) {
-            *reinterpret_cast<float4*>(&bv[k]) = *reinterpret_cast<const float4*>(bt + k);
-            *reinterpret_cast<float4*>(&cv[k]) = *reinterpret_cast<const float4*>(ct + k);
-          }
-        } else if constexpr (NS == 2) {
-          *reinterpret_cast<float2*>(bv) = *reinterpret_cast<const float2*>(bt);
-          *reinterpret_cast<float2*>(cv) = *reinterpret_cast<const float2*>(ct);
-        } else {
-#pragma unroll
-          for (int k = 0; k < NS; ++k) bv[k] = bt[k], cv[k] = ct[k];
-        }
-        if constexpr (NS == 1) {
-          h[0] = fmaf(ex2(st.x * A2[0]), h[0], st.z * bv[0]);
-          part[j] = cv[0] * h[0];
-        } else {
-          F2 y{0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < NS; k += 2) {
-            const F2 e = mul2(F2{st.x, st.y}, F2{A2[k], A2[k + 1]});
-            const F2 bx = mul2(F2{st.z, st.w}, F2{bv[k], bv[k + 1]});
-            const F2 hn = fma2(F2{ex2(e.x), ex2(e.y)}, F2{h[k], h[k + 1]}, bx);
-            h[k] = hn.x;
-            h[k + 1] = hn.y;
-            y = k == 0 ? mul2(F2{cv[0], cv[1]}, hn) : fma2(F2{cv[k], cv[k + 1]}, hn, y);
-          }
-          part[j] = y.x + y.y;
-        }
-      }
-#pragma unroll
-      for (int half = LPC / 2; half > 0; half /= 2) {
-        const bool up = (q & half) != 0;
-#pragma unroll
-        for (int j = 0; j < half; ++j) {
-          const float give = up ? part[j] : part[j + half], keep = up ? part[j + half] : part[j];
-          part[j] = keep + __shfl_xor_sync(0xffffffffu, give, half);
-        }
-      }
-      s_y[(tg + q) * YS + ch] = part[0];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < NX; ++k) {
-      const int i = tid + k * THREADS, t = i / (CB / V), c = i % (CB / V) * V;
-      if (i < TT * CB / V && t0 + t < len && c < nc) {
-        Pack<T, V> out;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float y = fmaf(s_D[c + e], to_f32(x[k].v[e]), s_y[t * YS + c + e]);
-          if (gate) y *= silu(to_f32(z[k].v[e]));
-          out.v[e] = from_f32<T>(y);
-        }
-        store_pack<T, V>(a.y.row(b, t0 + t) + c0 + c, out);
+      for (int w = 0; w < 2; ++w) {
+        rates(o[1 - w], e[1 - w]);
+        finish(k2, tg + w * U, o[w], e[w]);
+        read(k2, tg + (w + 2) * U, o[w]);
       }
     }
+    if (DEFER) store(k2, TT - U);
+    arrive_at(DONE + k2);
   }
   if (a.final_state && ch < nc) {
 #pragma unroll
     for (int k = 0; k < NS; ++k)
-      if (q * NS + k < a.N) a.final_state[at + q * NS + k] = h[k];
+      if (q * NS + k < a.N) a.final_state[((int64_t)b * a.C + c0 + ch) * a.N + q * NS + k] = h[k];
   }
 }
 
 template <typename T, int NS, int LPC>
 cudaError_t launch_as(Args<T> a, int64_t B, cudaStream_t st) {
-  a.blocks_per_group = (uint32_t)ceil_div(a.per_group, THREADS / LPC);
+  a.blocks_per_group = (uint32_t)ceil_div(a.per_group, LANES / LPC);
   const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group);
-  // 16-byte pieces: rows on 16 bytes, groups of channels and of states that are whole pieces
-  constexpr int V = 16 / (int)sizeof(T);
-  if constexpr (NS * LPC % V == 0) {
-    if (a.vec && a.per_group % V == 0 && a.N % V == 0) {
-      k_selective<T, NS, LPC, true><<<blocks, THREADS, 0, st>>>(a);
+  if constexpr (NS * LPC % (16 / (int)sizeof(T)) == 0) {
+    if (a.vec && a.bvec) {
+      k_selective<T, NS, LPC, true, true><<<blocks, THREADS, 0, st>>>(a);
       return cudaGetLastError();
     }
   }
-  k_selective<T, NS, LPC, false><<<blocks, THREADS, 0, st>>>(a);
+  if constexpr (NS > 1) {
+    if (a.vec)
+      k_selective<T, NS, LPC, true, false><<<blocks, THREADS, 0, st>>>(a);
+    else
+      k_selective<T, NS, LPC, false, false><<<blocks, THREADS, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_prompt(const Args<T>& a, int64_t B, cudaStream_t st) {
-  if (a.N <= 4) return launch_as<T, 4, 1>(a, B, st);
+cudaError_t launch_prompt(Args<T> a, int64_t B, cudaStream_t st) {
+  // rows on 16 bytes (vec, bvec as given) are moved in 16-byte pieces where groups of channels, and of states, are
+  // whole pieces too
+  constexpr int V = 16 / (int)sizeof(T);
+  a.vec = a.vec && a.per_group % V == 0;
+  a.bvec = a.bvec && a.N % V == 0;
+  if (a.N <= 4) return launch_as<T, 2, 2>(a, B, st);
   if (a.N <= 8) return launch_as<T, 4, 2>(a, B, st);
-  if (a.N <= 16) return launch_as<T, 4, 4>(a, B, st);
+  if (a.N <= 16) {
+    // More lanes per channel make more warps of a small problem, at more work per channel (each lane reads the step,
+    // sums are exchanged): 16 lanes while that is at most two warps per scheduler (768 channels of 2048 tokens 43 us,
+    // against 72 with 8 lanes and 98 with 4), 8 up to four (5120 channels 143 us against 163 with 4 lanes), 4 beyond
+    // (10240 channels 228 us against 238 with 8).  Not 16 where inputs come element by element, which its helpers
+    // cannot keep up with (128 channels, 512 tokens: 21 us with 8 lanes, 25 with 16).
+    const int64_t channels = B * a.C, warp = 32;
+    if (a.vec && a.bvec && channels * 16 <= 2 * SCHEDULERS * warp) return launch_as<T, 1, 16>(a, B, st);
+    if (channels * 8 <= 4 * SCHEDULERS * warp) return launch_as<T, 2, 8>(a, B, st);
+    return launch_as<T, 4, 4>(a, B, st);
+  }
   if (a.N <= 32) return launch_as<T, 4, 8>(a, B, st);
   if (a.N <= 64) return launch_as<T, 4, 16>(a, B, st);
   return launch_as<T, 8, 16>(a, B, st);
@@ -290,8 +433,8 @@ cudaError_t launch_prompt(const Args<T>& a, int64_t B, cudaStream_t st) {
 // One token: four state entries to a lane, a channel on ceil(N / 4) lanes
 // (rounded up to a power of two), y summed by shuffles.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(THREADS) k_selective_step(const Args<T> a, float* state, int lpc) {
-  const uint32_t i = (blockIdx.x * THREADS + threadIdx.x) / lpc;
+__global__ void __launch_bounds__(LANES) k_selective_step(const Args<T> a, float* state, int lpc) {
+  const uint32_t i = (blockIdx.x * LANES + threadIdx.x) / lpc;
   const int q = threadIdx.x % lpc;
   const bool on = i < a.total;
   const uint32_t j = on ? i : a.total - 1;  // lanes behind the end take part in the shuffles
@@ -308,7 +451,7 @@ __global__ void __launch_bounds__(THREADS) k_selective_step(const Args<T> a, flo
       const Pack<float, 4> hp = load_pack<float, 4>(st), rp = load_pack<float, 4>(ap);
       const Pack<T, 4> b4 = load_pack<T, 4>(bp), c4 = load_pack<T, 4>(cp);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = hp.v[k], A[k] = rp.v[k], bv[k] = to_f32(b4.v[k]), cv[k] = to_f32(c4.v[k]);
+      for (int k = 0; k < 4; ++k) h[k] = hp.get(k), A[k] = rp.get(k), bv[k] = b4.get(k), cv[k] = c4.get(k);
     }
   } else {
 #pragma unroll
@@ -329,7 +472,7 @@ __global__ void __launch_bounds__(THREADS) k_selective_step(const Args<T> a, flo
   for (int off = 1; off < lpc; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
   if (!on) return;
   if (VEC) {
-    if (some > 0) store_pack<float, 4>(st, Pack<float, 4>{{h[0], h[1], h[2], h[3]}});
+    if (some > 0) store_pack<float, 4>(st, to_pack<float, 4>(h));
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -347,14 +490,14 @@ cudaError_t launch_token(Args<T> a, float* state, int64_t B, cudaStream_t st) {
   int lpc = 1;
   while (lpc * 4 < a.N) lpc *= 2;
   a.total = (uint32_t)(B * a.C);
-  const unsigned blocks = (unsigned)ceil_div((int64_t)a.total * lpc, THREADS);
+  const unsigned blocks = (unsigned)ceil_div((int64_t)a.total * lpc, LANES);
   const uintptr_t f = reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(a.A);
   const uintptr_t t = reinterpret_cast<uintptr_t>(a.bm.p) | reinterpret_cast<uintptr_t>(a.cm.p) | a.bm.bs * sizeof(T);
   // four entries by one access: whole fours of states, on 16 bytes (B and C: on four elements)
   if (a.N % 4 == 0 && (f & 15) == 0 && (t & (4 * sizeof(T) - 1)) == 0)
-    k_selective_step<T, true><<<blocks, THREADS, 0, st>>>(a, state, lpc);
+    k_selective_step<T, true><<<blocks, LANES, 0, st>>>(a, state, lpc);
   else
-    k_selective_step<T, false><<<blocks, THREADS, 0, st>>>(a, state, lpc);
+    k_selective_step<T, false><<<blocks, LANES, 0, st>>>(a, state, lpc);
   return cudaGetLastError();
 }
 
@@ -427,8 +570,9 @@ ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream
     a.softplus = (d->flags & SSD_SELECTIVE_SOFTPLUS) != 0;
     if (k.state) return launch_token<T>(a, k.state, B, st);
     a.vec = true;
-    for (const RowArg* r : {&k.x, &k.dt, &k.z, &k.bm, &k.cm, &k.y})
+    for (const RowArg* r : {&k.x, &k.dt, &k.z, &k.y})
       if (r->p && !rows_on_16(*r, B, L, es)) a.vec = false;
+    a.bvec = rows_on_16(k.bm, B, L, es) && rows_on_16(k.cm, B, L, es);
     return launch_prompt<T>(a, B, st);
   };
   return cuda_status(d->io_dtype == SSD_BF16 ? go(__nv_bfloat16()) : go(float()));

@@ -417,90 +417,91 @@ def ssd_step(x, dt, A, Bm, Cm, state, D=None, y=None, stream=None, input_dt: boo
 
 
 # ---- the layer around and beside the scan -------------------------------------------------
+#
+# A single token is a few microseconds of GPU time, so these bindings look at each tensor once: the checks hand back
+# what the call takes (address and strides).
 
-def _rows(x: torch.Tensor, shape, *ts):
-    """Checks the io tensors of a call beside its first, `x`: each None or of
-    `shape`, of x's dtype, on x's device, and with dense channels (as x itself)."""
-    dev, dtype = x.device, x.dtype
-    if dev.type != "cuda":
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_of(x: torch.Tensor) -> int:
+    dev = x.get_device()
+    if dev < 0:
         raise SSDError(1, "tensors must be on a CUDA device")
-    for t in (x,) + ts:
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise SSDError(2, f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise SSDError(3, f"expected {dtype}, got {t.dtype}")
-        if t.device != dev:
-            raise SSDError(1, "tensors on different devices")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise SSDError(2, "each token's channels must be dense")
+    return dev
 
 
-def _whole(x: torch.Tensor, dtype, *pairs):
-    """Checks contiguous tensors (parameters, states): pairs of (tensor or None, shape)."""
-    for t, shape in pairs:
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise SSDError(2, f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise SSDError(3, f"expected {dtype}, got {t.dtype}")
-        if t.device != x.device:
-            raise SSDError(1, "tensors on different devices")
-        if not t.is_contiguous():
-            raise SSDError(1, "tensors must be contiguous")
+def _mismatch(t: torch.Tensor, shape, dtype, dev: int):
+    if t.shape != shape:
+        raise SSDError(2, f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise SSDError(3, f"expected {dtype}, got {t.dtype}")
+    raise SSDError(1, "tensors on different devices" if t.get_device() != dev else "tensors must be contiguous")
 
 
-def _groups(x: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor):
-    """(G, N) of the B and C that go with x ([..., C] to [..., G, N])."""
-    if Bm.dim() != x.dim() + 1 or Bm.shape[:-2] != x.shape[:-1] or Cm.shape != Bm.shape:
-        raise SSDError(2, f"B and C must be {tuple(x.shape[:-1])} + (G, N)")
+def _rows(t: Optional[torch.Tensor], shape, dtype, dev: int, outer: tuple):
+    """Address and outer strides of an io tensor: None or of `shape`, `dtype` and device, with dense channels.
+    `outer`: what stands for the strides of None."""
+    if t is None:
+        return (None,) + outer
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _mismatch(t, shape, dtype, dev)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise SSDError(2, "each token's channels must be dense")
+    return (t.data_ptr(),) + st[:-1]
+
+
+def _whole(t: Optional[torch.Tensor], shape, dtype, dev: int):
+    """Address of a parameter or state: None or of `shape`, `dtype` and device, contiguous."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _mismatch(t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _groups(x: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor, dev: int):
+    """(G, N), addresses and outer strides of the B and C that go with x ([..., C] to [..., G, N])."""
+    shape, lead = Bm.shape, x.shape[:-1]
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead or Cm.shape != shape:
+        raise SSDError(2, f"B and C must be {tuple(lead)} + (G, N)")
     if Bm.dtype != x.dtype or Cm.dtype != x.dtype:
         raise SSDError(3, f"expected {x.dtype}, got {Bm.dtype} and {Cm.dtype}")
-    if Bm.device != x.device or Cm.device != x.device:
+    if Bm.get_device() != dev or Cm.get_device() != dev:
         raise SSDError(1, "tensors on different devices")
-    G, N = Bm.shape[-2:]
+    G, N = shape[-2:]
     sb, sc = Bm.stride(), Cm.stride()
-    if sb != sc and any(n > 1 and i != j for n, i, j in zip(Bm.shape, sb, sc)):
+    if sb != sc and any(n > 1 and i != j for n, i, j in zip(shape, sb, sc)):
         raise SSDError(2, "B and C must have the same strides")
     if (N > 1 and sb[-1] != 1) or (G > 1 and sb[-2] != N):
         raise SSDError(2, "each token's groups must be dense")
-    return G, N
+    return G, N, Bm.data_ptr(), Cm.data_ptr(), sb[:-2]
 
 
-def _call(name: str, x: torch.Tensor, stream, *args):
-    """One entry point on x's device and `stream` (default: that device's current one)."""
+def _call(name: str, dev: int, stream, *args):
+    """One entry point on device `dev` and `stream` (default: that device's current one)."""
     if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        handle = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     fn = getattr(_lib or lib(), name)
-    if x.device.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         s = fn(*args, handle)
     else:
-        with torch.cuda.device(x.device):
+        with torch.cuda.device(dev):
             s = fn(*args, handle)
     if s != 0:
         _check(s, name)
 
 
-def _at(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _at3(t: Optional[torch.Tensor]):
-    """Pointer, batch stride and token stride of a [B, L, ...] tensor."""
-    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _at2(t: Optional[torch.Tensor]):
-    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
-
-
-def _new_rows(x: torch.Tensor, lengths):
+def _new_rows(x: torch.Tensor, lengths=None):
     # rows behind a padded sequence are not written: zeros there, not what memory held
-    make = torch.empty if lengths is None else torch.zeros
-    return make(x.shape, dtype=x.dtype, device=x.device)
+    make = torch.empty_like if lengths is None else torch.zeros_like
+    return make(x, memory_format=torch.contiguous_format)
+
+
+_NONE2, _NONE1 = (0, 0), (0,)
 
 
 def ssd_conv_fwd(x, weight, bias=None, init_state=None, lengths=None, silu: bool = True, y=None, final_state=None,
@@ -510,38 +511,39 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, lengths=None, silu: bool
     token (None: zeros); lengths [B] int32 the tokens of each sequence of a padded batch.
     Returns (y, final_state [B,W-1,C] or None); final_state may be init_state itself.  A y given by the
     caller keeps its rows behind each sequence; one made here has zeros there."""
-    if x.dim() != 3 or weight.dim() != 2:
+    shape = x.shape
+    if len(shape) != 3 or weight.dim() != 2:
         raise SSDError(2, "x must be [B,L,C] and weight [C,W]")
-    Bz, L, C = x.shape
+    Bz, L, C = shape
     W = weight.shape[1]
-    _rows(x, x.shape, y)
-    _whole(x, torch.float32, (weight, (C, W)), (bias, (C,)))
-    _whole(x, x.dtype, (init_state, (Bz, W - 1, C)), (final_state, (Bz, W - 1, C)))
-    _whole(x, torch.int32, (lengths, (Bz,)))
-    dims = ConvDims(Bz, L, C, W, _io_code(x), int(silu))
+    dev, io, f32 = _device_of(x), x.dtype, torch.float32
     if y is None:
         y = _new_rows(x, lengths)
     if final_state is None and want_final:
-        final_state = torch.empty((Bz, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
-    _call("ssd_conv_fwd", x, stream, ctypes.byref(dims), *_at3(x), _at(weight), _at(bias), _at(init_state),
-          _at(lengths), *_at3(y), _at(final_state))
+        final_state = torch.empty((Bz, max(W - 1, 0), C), dtype=io, device=x.device)
+    dims = ConvDims(Bz, L, C, W, _io_code(x), int(silu))
+    _call("ssd_conv_fwd", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE2),
+          _whole(weight, (C, W), f32, dev), _whole(bias, (C,), f32, dev), _whole(init_state, (Bz, W - 1, C), io, dev),
+          _whole(lengths, (Bz,), torch.int32, dev), *_rows(y, shape, io, dev, _NONE2),
+          _whole(final_state, (Bz, W - 1, C), io, dev))
     return y, final_state
 
 
 def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream=None):
     """One token of the convolution: x [B,C], state [B,W-1,C] (the last inputs, shifted by x in place).
     Returns y [B,C]."""
-    if x.dim() != 2 or weight.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2 or weight.dim() != 2:
         raise SSDError(2, "x must be [B,C] and weight [C,W]")
-    Bz, C = x.shape
+    Bz, C = shape
     W = weight.shape[1]
-    _rows(x, x.shape, y)
-    _whole(x, torch.float32, (weight, (C, W)), (bias, (C,)))
-    _whole(x, x.dtype, (state, (Bz, W - 1, C)))
-    dims = ConvDims(Bz, 1, C, W, _io_code(x), int(silu))
+    dev, io, f32 = _device_of(x), x.dtype, torch.float32
     if y is None:
-        y = torch.empty((Bz, C), dtype=x.dtype, device=x.device)
-    _call("ssd_conv_step", x, stream, ctypes.byref(dims), *_at2(x), _at(weight), _at(bias), _at(state), *_at2(y))
+        y = _new_rows(x)
+    dims = ConvDims(Bz, 1, C, W, _io_code(x), int(silu))
+    _call("ssd_conv_step", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE1),
+          _whole(weight, (C, W), f32, dev), _whole(bias, (C,), f32, dev), _whole(state, (Bz, W - 1, C), io, dev),
+          *_rows(y, shape, io, dev, _NONE1))
     return y
 
 
@@ -552,21 +554,22 @@ def ssd_selective_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state
     (softplus=False: dt + dt_bias), y is gated by silu(z) where z is given.  init_state [B,C,N] f32
     (None: zeros), lengths [B] int32 as in ssd_conv_fwd.  Returns (y, final_state [B,C,N] or None);
     final_state may be init_state itself."""
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise SSDError(2, "x must be [B,L,C]")
-    Bz, L, C = x.shape
-    _rows(x, x.shape, dt, z, y)
-    G, N = _groups(x, Bm, Cm)
-    _whole(x, torch.float32, (A, (C, N)), (D, (C,)), (dt_bias, (C,)), (init_state, (Bz, C, N)),
-           (final_state, (Bz, C, N)))
-    _whole(x, torch.int32, (lengths, (Bz,)))
-    dims = SelectiveDims(Bz, L, C, N, G, _io_code(x), int(softplus))
+    Bz, L, C = shape
+    dev, io, f32 = _device_of(x), x.dtype, torch.float32
+    G, N, at_b, at_c, bc = _groups(x, Bm, Cm, dev)
     if y is None:
         y = _new_rows(x, lengths)
     if final_state is None and want_final:
-        final_state = torch.empty((Bz, C, N), dtype=torch.float32, device=x.device)
-    _call("ssd_selective_fwd", x, stream, ctypes.byref(dims), *_at3(x), *_at3(dt), _at(A), _at(Bm), *_at3(Cm),
-          _at(D), *_at3(z), _at(dt_bias), _at(init_state), _at(lengths), *_at3(y), _at(final_state))
+        final_state = torch.empty((Bz, C, N), dtype=f32, device=x.device)
+    dims = SelectiveDims(Bz, L, C, N, G, _io_code(x), int(softplus))
+    _call("ssd_selective_fwd", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE2),
+          *_rows(dt, shape, io, dev, _NONE2), _whole(A, (C, N), f32, dev), at_b, at_c, *bc, _whole(D, (C,), f32, dev),
+          *_rows(z, shape, io, dev, _NONE2), _whole(dt_bias, (C,), f32, dev),
+          _whole(init_state, (Bz, C, N), f32, dev), _whole(lengths, (Bz,), torch.int32, dev),
+          *_rows(y, shape, io, dev, _NONE2), _whole(final_state, (Bz, C, N), f32, dev))
     return y, final_state
 
 
@@ -574,33 +577,40 @@ def ssd_selective_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, so
                        stream=None):
     """One token of the selective scan: x, dt, z [B,C], Bm, Cm [B,G,N], state [B,C,N] f32 (updated in
     place).  Returns y [B,C]."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise SSDError(2, "x must be [B,C]")
-    Bz, C = x.shape
-    _rows(x, x.shape, dt, z, y)
-    G, N = _groups(x, Bm, Cm)
-    _whole(x, torch.float32, (A, (C, N)), (D, (C,)), (dt_bias, (C,)), (state, (Bz, C, N)))
-    dims = SelectiveDims(Bz, 1, C, N, G, _io_code(x), int(softplus))
+    Bz, C = shape
+    dev, io, f32 = _device_of(x), x.dtype, torch.float32
+    G, N, at_b, at_c, bc = _groups(x, Bm, Cm, dev)
     if y is None:
-        y = torch.empty((Bz, C), dtype=x.dtype, device=x.device)
-    _call("ssd_selective_step", x, stream, ctypes.byref(dims), *_at2(x), *_at2(dt), _at(A), _at(Bm), *_at2(Cm),
-          _at(D), *_at2(z), _at(dt_bias), _at(state), *_at2(y))
+        y = _new_rows(x)
+    dims = SelectiveDims(Bz, 1, C, N, G, _io_code(x), int(softplus))
+    _call("ssd_selective_step", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE1),
+          *_rows(dt, shape, io, dev, _NONE1), _whole(A, (C, N), f32, dev), at_b, at_c, *bc, _whole(D, (C,), f32, dev),
+          *_rows(z, shape, io, dev, _NONE1), _whole(dt_bias, (C,), f32, dev), _whole(state, (Bz, C, N), f32, dev),
+          *_rows(y, shape, io, dev, _NONE1))
     return y
 
 
 def ssd_rmsnorm_gated(x, z=None, weight=None, eps: float = 1e-5, ngroups: int = 1, out=None, stream=None):
     """out = weight u / sqrt(mean(u^2) + eps) with u = x silu(z) (u = x without z), the mean over each of
     `ngroups` runs of features; x, z [B,L,F] or [B,F] with any row strides, weight [F] f32.  out may be x."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise SSDError(2, "x must be [B,L,F] or [B,F]")
-    F = x.shape[-1]
-    _rows(x, x.shape, z, out)
-    _whole(x, torch.float32, (weight, (F,)))
-    dims = NormDims(x.shape[0], x.shape[1] if x.dim() == 3 else 1, F, int(ngroups), _io_code(x), 0)
+    F = shape[-1]
+    dev, io = _device_of(x), x.dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    at = _at3 if x.dim() == 3 else (lambda t: _at2(t) + (0,))
-    _call("ssd_rmsnorm_gated", x, stream, ctypes.byref(dims), *at(x), *at(z), _at(weight), float(eps), *at(out))
+        out = _new_rows(x)
+    if len(shape) == 3:
+        L, none, last = shape[1], _NONE2, ()
+    else:
+        L, none, last = 1, _NONE1, _NONE1  # one token per row: its stride is not looked at
+    dims = NormDims(shape[0], L, F, int(ngroups), _io_code(x), 0)
+    _call("ssd_rmsnorm_gated", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, none), *last,
+          *_rows(z, shape, io, dev, none), *last, _whole(weight, (F,), torch.float32, dev), float(eps),
+          *_rows(out, shape, io, dev, none), *last)
     return out
 
 
