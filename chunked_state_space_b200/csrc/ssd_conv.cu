@@ -8,14 +8,14 @@
 // A thread owns 16 bytes of channels (one element where rows are not 16-byte
 // aligned) and a run of consecutive tokens, and keeps the last W-1 inputs in
 // registers, so a tap costs no further load; only the W-1 rows before a run
-// are read twice.  Eight rows are loaded before the first is used.
+// are read twice.
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace conv {
 
 constexpr int THREADS = 128;
-constexpr int AHEAD = 8;  // rows in flight per thread
+constexpr int AHEAD = 4;  // rows that a thread loads before it computes the AHEAD before them
 
 template <typename T>
 struct Args {
@@ -35,12 +35,15 @@ template <int W, int VEC, bool SILU>
 struct Taps {
   float w[W][VEC], b[VEC];
   __device__ __forceinline__ void load(const float* weight, const float* bias, int64_t c) {
+    float rows[VEC * W];
+    load_params<VEC * W, (VEC > 1)>(weight + c * W, rows);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[k][i] = weight[(c + i) * W + k];
-      b[i] = bias ? bias[c + i] : 0.f;
+      for (int k = 0; k < W; ++k) w[k][i] = rows[i * W + k];
+      b[i] = 0.f;
     }
+    if (bias) load_params<VEC, (VEC > 1)>(bias + c, b);
   }
   // old[0] is the oldest of the W-1 inputs before `in`
   template <typename T>
@@ -125,43 +128,62 @@ __global__ void __launch_bounds__(THREADS, 4) k_conv_fwd(const Args<T> a) {
     }
   };
   int64_t t = t0;
-#pragma unroll 1
-  for (; t + AHEAD <= t1; t += AHEAD) {
-    Pack<T, VEC> in[AHEAD];
+  if (t + AHEAD <= t1) {
+    Pack<T, VEC> in[AHEAD], next[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j, x += a.x.ts) in[j] = load_pack<T, VEC>(x);
+#pragma unroll 1
+    for (; t + AHEAD <= t1; t += AHEAD) {
+      if (t + 2 * AHEAD <= t1) {
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) token(in[j]);
+        for (int j = 0; j < AHEAD; ++j, x += a.x.ts) next[j] = load_pack<T, VEC>(x);
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) token(in[j]);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) in[j] = next[j];
+    }
   }
 #pragma unroll 1
   for (; t < t1; ++t, x += a.x.ts) token(load_pack<T, VEC>(x));
 }
 
-template <typename T, int W, int VEC, bool SILU>
+// One token: a thread takes 16 bytes of channels (or one) of up to ROWS
+// sequences, with their weights loaded once.
+template <typename T, int W, int VEC, bool SILU, int ROWS>
 __global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, int64_t xbs, const float* weight,
                                                        const float* bias, T* state, T* __restrict__ y, int64_t ybs,
-                                                       int64_t C, uint32_t nvec, uint32_t total) {
+                                                       int64_t B, int64_t C, uint32_t nvec, uint32_t total) {
   const uint32_t idx = blockIdx.x * THREADS + threadIdx.x;
   if (idx >= total) return;
-  const uint32_t b32 = idx / nvec;
-  const int64_t b = b32, c = (int64_t)(idx - b32 * nvec) * VEC;
-  T* st = state + b * (W - 1) * C + c;
-  Pack<T, VEC> seen[W];
+  const uint32_t r = idx / nvec;
+  const int64_t b0 = (int64_t)r * ROWS, c = (int64_t)(idx - r * nvec) * VEC;
+  Pack<T, VEC> seen[ROWS][W];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) seen[k] = load_pack<T, VEC>(st + k * C);
-  seen[W - 1] = load_pack<T, VEC>(x + b * xbs + c);
+  for (int j = 0; j < ROWS; ++j) {
+    if (b0 + j < B) {
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) seen[j][k] = load_pack<T, VEC>(state + ((b0 + j) * (W - 1) + k) * C + c);
+      seen[j][W - 1] = load_pack<T, VEC>(x + (b0 + j) * xbs + c);
+    }
+  }
   Taps<W, VEC, SILU> taps;
   taps.load(weight, bias, c);
-  float old[W - 1][VEC], cur[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
+  for (int j = 0; j < ROWS; ++j) {
+    if (b0 + j < B) {
+      float old[W - 1][VEC], cur[VEC];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) old[k][i] = seen[k].get(i);
-    cur[i] = seen[W - 1].get(i);
+      for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) old[k][i] = seen[j][k].get(i);
+        cur[i] = seen[j][W - 1].get(i);
+      }
+      store_pack<T, VEC>(y + (b0 + j) * ybs + c, taps.template apply<T>(old, cur));
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) store_pack<T, VEC>(state + ((b0 + j) * (W - 1) + k) * C + c, seen[j][k + 1]);
+    }
   }
-  store_pack<T, VEC>(y + b * ybs + c, taps.template apply<T>(old, cur));
-#pragma unroll
-  for (int k = 0; k < W - 1; ++k) store_pack<T, VEC>(st + k * C, seen[k + 1]);
 }
 
 // Tokens per thread: as many as leave every SM about 1024 threads (the rows
@@ -193,14 +215,24 @@ cudaError_t launch(const Args<T>& a0, bool use_silu, cudaStream_t st) {
 template <typename T, int W, int VEC>
 cudaError_t launch_step(const ssd_conv_dims* d, const void* x, int64_t xbs, const float* weight, const float* bias,
                         void* state, void* y, int64_t ybs, cudaStream_t st) {
-  const uint32_t nvec = (uint32_t)(d->channels / VEC), total = (uint32_t)(d->batch * nvec);
-  const unsigned blocks = (total + THREADS - 1) / THREADS;
+  const int64_t nvec = d->channels / VEC;
+  auto go = [&](auto silu, auto rows) {
+    const uint32_t total = (uint32_t)(ceil_div(d->batch, rows.value) * nvec);
+    k_conv_step<T, W, VEC, silu.value, rows.value><<<(total + THREADS - 1) / THREADS, THREADS, 0, st>>>(
+        (const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs, d->batch, d->channels, (uint32_t)nvec, total);
+  };
+  // four sequences a thread where that still makes a block for every SM
+  const bool many = ceil_div(d->batch, 4) * nvec >= 148 * THREADS;
+  auto pick = [&](auto silu) {
+    if (many)
+      go(silu, std::integral_constant<int, 4>());
+    else
+      go(silu, std::integral_constant<int, 1>());
+  };
   if (d->flags & SSD_CONV_SILU)
-    k_conv_step<T, W, VEC, true><<<blocks, THREADS, 0, st>>>((const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs,
-                                                             d->channels, nvec, total);
+    pick(std::true_type());
   else
-    k_conv_step<T, W, VEC, false><<<blocks, THREADS, 0, st>>>((const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs,
-                                                              d->channels, nvec, total);
+    pick(std::false_type());
   return cudaGetLastError();
 }
 
@@ -261,7 +293,7 @@ extern "C" ssd_status ssd_conv_fwd(const ssd_conv_dims* d, const void* x, int64_
   if (spans_meet(sy, si) || spans_meet(sy, sf) || (final_state != init_state && spans_meet(sf, si)))
     return SSD_ERR_INVALID_ARG;
   const bool vec = rows_on_16(rx, B, L, es) && rows_on_16(ry, B, L, es) && rows_on_16(ri, B, W - 1, es) &&
-                   rows_on_16(rf, B, W - 1, es);
+                   rows_on_16(rf, B, W - 1, es) && on_16(weight) && on_16(bias);
   return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
     using T = decltype(t);
     conv::Args<T> a{};
@@ -295,7 +327,8 @@ extern "C" ssd_status ssd_conv_step(const ssd_conv_dims* d, const void* x, int64
   for (const Span& in : {sx, sw, sb})
     if (spans_meet(sy, in) || spans_meet(ss, in)) return SSD_ERR_INVALID_ARG;
   if (spans_meet(sy, ss)) return SSD_ERR_INVALID_ARG;
-  const bool vec = rows_on_16(rx, B, 1, es) && rows_on_16(ry, B, 1, es) && rows_on_16(rs, B, W - 1, es);
+  const bool vec = rows_on_16(rx, B, 1, es) && rows_on_16(ry, B, 1, es) && rows_on_16(rs, B, W - 1, es) &&
+                   on_16(weight) && on_16(bias);
   return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
     return conv::launch_step<decltype(t), w.value, v.value>(d, x, x_bstride, weight, bias, state, y, y_bstride,
                                                             static_cast<cudaStream_t>(stream));

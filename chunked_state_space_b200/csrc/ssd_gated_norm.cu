@@ -2,8 +2,9 @@
 //   u = x silu(z);  out = weight u / sqrt(mean over the feature's group of u^2 + eps)
 // Bound by HBM: x and z are read once and out is written once.  A run of
 // features (one group of one row) is held in registers as u between the sum
-// and the scaling, PER 16-byte pieces per thread, all loaded before the first
-// is used; the sum of squares is f32 and reduced in a fixed order.
+// and the scaling, PER 16-byte pieces per thread; blocks stay for many rows,
+// with their weights in registers and the next row's loads under way while
+// this one's sum is reduced.  The sum of squares is f32, in a fixed order.
 #include "ssd_rows.cuh"
 
 namespace ssd {
@@ -18,9 +19,9 @@ struct Args {
   Rows<T> out;
   const float* weight;
   float eps;
-  int64_t runs;      // rows * groups
-  uint32_t groups, L;
-  int64_t n;         // features of a group
+  int64_t rows;
+  uint32_t L;
+  int64_t n;  // features of a group
 };
 
 template <typename T, int VEC>
@@ -29,81 +30,126 @@ __device__ __forceinline__ void gated(const Pack<T, VEC>& x, const Pack<T, VEC>&
   for (int i = 0; i < VEC; ++i) u[i] = gate ? x.get(i) * silu(z.get(i)) : x.get(i);
 }
 
-// One run per warp (BLOCK false, four warps of a block on four runs) or per block.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Runs of group blockIdx.y, one at a time per warp (BLOCK false) or block.
 template <typename T, int VEC, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T> a) {
-  __shared__ float part[32];
+  __shared__ float part[2][MOST / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t run = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-  if (run >= a.runs) return;
   const int me = BLOCK ? (int)threadIdx.x : lane, all = BLOCK ? (int)blockDim.x : 32;
-  const int64_t r = run / a.groups, g = run - r * a.groups;
-  const int64_t b = r / a.L, t = r - b * a.L;
-  const T* x = a.x.row(b, t) + g * a.n;
+  const int64_t g0 = (int64_t)blockIdx.y * a.n;  // the group's first feature
+  const int pieces = (int)(a.n / VEC);
   const bool gate = a.z.p != nullptr;
-  const T* z = gate ? a.z.row(b, t) + g * a.n : x;
-  T* out = a.out.row(b, t) + g * a.n;
-  const int64_t pieces = a.n / VEC;
-  float u[PER][VEC];
-  float ss = 0.f;
-  for (int64_t p0 = 0; p0 < pieces; p0 += (int64_t)PER * all) {
-    Pack<T, VEC> px[PER], pz[PER];
+  int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  const int64_t step = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
+  float w[PER][VEC];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[k][i] = 1.f;
+    if (a.weight && me + k * all < pieces) load_params<VEC, (VEC > 1)>(a.weight + g0 + (int64_t)(me + k * all) * VEC, w[k]);
+  }
+  Pack<T, VEC> x[PER], z[PER];
+  auto fetch = [&](int64_t r) {
+    const int64_t b = r / a.L, t = r - b * a.L;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t p = p0 + me + k * all;
+      const int p = me + k * all;
       if (p < pieces) {
-        px[k] = load_pack<T, VEC>(x + p * VEC);
-        pz[k] = load_pack<T, VEC>(z + p * VEC);
+        x[k] = load_pack<T, VEC>(a.x.row(b, t) + g0 + (int64_t)p * VEC);
+        if (gate) z[k] = load_pack<T, VEC>(a.z.row(b, t) + g0 + (int64_t)p * VEC);
       }
     }
+  };
+  if (row < a.rows) fetch(row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    float u[PER][VEC];
+    float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      if (p0 + me + k * all < pieces) {
-        gated(px[k], pz[k], gate, u[k]);
+      if (me + k * all < pieces) {
+        gated(x[k], z[k], gate, u[k]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) ss = fmaf(u[k][i], u[k][i], ss);
       }
     }
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  if (BLOCK) {
-    if (lane == 0) part[warp] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int w = 0; w < all / 32; ++w) ss += part[w];
-  }
-  const float inv = 1.0f / sqrtf(ss / (float)a.n + a.eps);
-  for (int64_t p0 = 0; p0 < pieces; p0 += (int64_t)PER * all) {
+    if (row + step < a.rows) fetch(row + step);
+    ss = warp_sum(ss);
+    if (BLOCK) {
+      // two sets of sums in turn: a warp that is a row ahead does not write over what another still reads
+      if (lane == 0) part[turn][warp] = ss;
+      __syncthreads();
+      ss = 0.f;
+      for (int k = 0; k < all / 32; ++k) ss += part[turn][k];
+    }
+    const float inv = 1.0f / sqrtf(ss / (float)a.n + a.eps);
+    const int64_t b = row / a.L, t = row - b * a.L;
+    T* out = a.out.row(b, t) + g0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t p = p0 + me + k * all;
+      const int p = me + k * all;
       if (p < pieces) {
-        // a run longer than the registers hold is read again
-        if (pieces > (int64_t)PER * all) gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u[k]);
         float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float w = a.weight ? a.weight[g * a.n + p * VEC + i] : 1.f;
-          o[i] = u[k][i] * inv * w;
-        }
-        store_pack<T, VEC>(out + p * VEC, to_pack<T, VEC>(o));
+        for (int i = 0; i < VEC; ++i) o[i] = u[k][i] * inv * w[k][i];
+        store_pack<T, VEC>(out + (int64_t)p * VEC, to_pack<T, VEC>(o));
       }
     }
   }
 }
 
-// A run of up to 32 * PER pieces takes a warp, a longer one a block of as many
-// warps as hold it (at most MOST threads; a run beyond them is read twice).
+// A run longer than the registers of a block hold: read twice.
 template <typename T, int VEC>
-cudaError_t launch(const Args<T>& a, cudaStream_t st) {
+__global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
+  __shared__ float part[MOST / 32];
+  const int64_t row = blockIdx.x, b = row / a.L, t = row - b * a.L, g0 = (int64_t)blockIdx.y * a.n;
+  const bool gate = a.z.p != nullptr;
+  const T* x = a.x.row(b, t) + g0;
+  const T* z = gate ? a.z.row(b, t) + g0 : x;
+  T* out = a.out.row(b, t) + g0;
   const int64_t pieces = a.n / VEC;
+  float u[VEC], ss = 0.f;
+  for (int64_t p = threadIdx.x; p < pieces; p += MOST) {
+    gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) ss = fmaf(u[i], u[i], ss);
+  }
+  ss = warp_sum(ss);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = 0.f;
+  for (int k = 0; k < MOST / 32; ++k) ss += part[k];
+  const float inv = 1.0f / sqrtf(ss / (float)a.n + a.eps);
+  for (int64_t p = threadIdx.x; p < pieces; p += MOST) {
+    gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u);
+    float w[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = 1.f;
+    if (a.weight) load_params<VEC, (VEC > 1)>(a.weight + g0 + p * VEC, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) u[i] *= inv * w[i];
+    store_pack<T, VEC>(out + p * VEC, to_pack<T, VEC>(u));
+  }
+}
+
+// A run of up to 32 * PER pieces takes a warp, a longer one a block of as many
+// warps as hold it; the grid is what the SMs hold at 128 registers a thread.
+template <typename T, int VEC>
+cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
+  const int64_t pieces = a.n / VEC;
+  auto blocks = [](int64_t want, int64_t most) { return (unsigned)(want < most ? want : most); };
   if (pieces <= 32 * PER) {
-    k_gated_norm<T, VEC, false><<<(unsigned)ceil_div(a.runs, 4), 128, 0, st>>>(a);
+    k_gated_norm<T, VEC, false><<<dim3(blocks(ceil_div(a.rows, 4), 148 * 4), groups), 128, 0, st>>>(a);
+  } else if (pieces <= MOST * PER) {
+    const int64_t threads = ceil_div(ceil_div(pieces, PER), 32) * 32;
+    k_gated_norm<T, VEC, true><<<dim3(blocks(a.rows, 148 * (512 / threads)), groups), (unsigned)threads, 0, st>>>(a);
   } else {
-    int64_t threads = ceil_div(ceil_div(pieces, PER), 32) * 32;
-    if (threads > MOST) threads = MOST;
-    k_gated_norm<T, VEC, true><<<(unsigned)a.runs, (unsigned)threads, 0, st>>>(a);
+    k_gated_norm_long<T, VEC><<<dim3((unsigned)a.rows, groups), MOST, 0, st>>>(a);
   }
   return cudaGetLastError();
 }
@@ -119,7 +165,7 @@ extern "C" ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, i
   if (d->io_dtype != SSD_F32 && d->io_dtype != SSD_BF16) return SSD_ERR_DTYPE;
   const int64_t B = d->batch, L = d->seqlen, F = d->features, G = d->ngroups;
   if (B < 1 || L < 1 || F < 1 || G < 1 || F % G != 0) return SSD_ERR_SHAPE;
-  if (B > 0x7fffffff || L > 0x7fffffff || F > 0x7fffffff || B * L > 0x7fffffff / G) return SSD_ERR_UNSUPPORTED;
+  if (B > 0x7fffffff || L > 0x7fffffff || F > 0x7fffffff || B * L > 0x7fffffff || G > 65535) return SSD_ERR_UNSUPPORTED;
   if (!x || !out || !(eps >= 0.0f)) return SSD_ERR_INVALID_ARG;
   const size_t es = io_bytes(d->io_dtype);
   const RowArg rx{x, x_bstride, x_tstride, F}, rz{z, z_bstride, z_tstride, F}, ro{out, out_bstride, out_tstride, F};
@@ -132,7 +178,7 @@ extern "C" ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, i
   const bool in_place = x == out && (B == 1 || x_bstride == out_bstride) && (L == 1 || x_tstride == out_tstride);
   if ((!in_place && spans_meet(so, sx)) || spans_meet(so, sz) || spans_meet(so, sw)) return SSD_ERR_INVALID_ARG;
   bool vec = rows_on_16(rx, B, L, es) && rows_on_16(ro, B, L, es) && (!z || rows_on_16(rz, B, L, es));
-  vec = vec && (F / G * es) % 16 == 0;
+  vec = vec && (F / G * es) % 16 == 0 && on_16(weight);
   auto go = [&](auto t, auto v) {
     using T = decltype(t);
     gnorm::Args<T> a{};
@@ -141,11 +187,10 @@ extern "C" ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, i
     a.out = Rows<T>{(T*)out, out_bstride, out_tstride};
     a.weight = weight;
     a.eps = eps;
-    a.groups = (uint32_t)G;
     a.L = (uint32_t)L;
-    a.runs = B * L * G;
+    a.rows = B * L;
     a.n = F / G;
-    return gnorm::launch<T, v.value>(a, static_cast<cudaStream_t>(stream));
+    return gnorm::launch<T, v.value>(a, (unsigned)G, static_cast<cudaStream_t>(stream));
   };
   if (d->io_dtype == SSD_BF16)
     return cuda_status(vec ? go(__nv_bfloat16(), std::integral_constant<int, 8>())

@@ -145,6 +145,18 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b,
   return n < 0 ? 0 : n > L ? L : n;
 }
 
+// N consecutive f32 parameters; ALIGNED: N is a multiple of 4 and p on 16 bytes.
+template <int N, bool ALIGNED>
+__device__ __forceinline__ void load_params(const float* p, float (&v)[N]) {
+  if constexpr (ALIGNED) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(&v[i]) = *reinterpret_cast<const float4*>(p + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
+  }
+}
+
 // Host side: what an entry point knows of one tensor of rows.
 struct RowArg {
   const void* p;
@@ -187,6 +199,7 @@ inline bool spans_meet(const Span& a, const Span& b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 
+inline bool on_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool f32_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace ssd

@@ -431,74 +431,98 @@ cudaError_t launch_prompt(Args<T> a, int64_t B, cudaStream_t st) {
 }
 
 // One token: four state entries to a lane, a channel on ceil(N / 4) lanes
-// (rounded up to a power of two), y summed by shuffles.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(LANES) k_selective_step(const Args<T> a, float* state, int lpc) {
+// (rounded up to a power of two), y summed by shuffles.  A lane takes its
+// channel of up to ROWS sequences, whose states it loads before the first is
+// used, with A, D and the bias loaded once.
+template <typename T, bool VEC, int ROWS>
+__global__ void __launch_bounds__(LANES) k_selective_step(const Args<T> a, float* state, int64_t B, int lpc) {
   const uint32_t i = (blockIdx.x * LANES + threadIdx.x) / lpc;
   const int q = threadIdx.x % lpc;
   const bool on = i < a.total;
   const uint32_t j = on ? i : a.total - 1;  // lanes behind the end take part in the shuffles
-  const uint32_t b = j / a.C;
-  const int c = (int)(j - b * a.C), n0 = q * 4, some = min(4, a.N - n0);
+  const uint32_t r = j / a.C;
+  const int64_t b0 = (int64_t)r * ROWS;
+  const int c = (int)(j - r * a.C), n0 = q * 4, some = min(4, a.N - n0);
   const int64_t gn = (int64_t)(c / a.per_group) * a.N + n0;
-  float h[4] = {}, A[4] = {}, bv[4] = {}, cv[4] = {};
-  float* st = state + (int64_t)j * a.N + n0;
-  const float* ap = a.A + (int64_t)c * a.N + n0;
-  const T* bp = a.bm.row(b, 0) + gn;
-  const T* cp = a.cm.row(b, 0) + gn;
-  if (VEC) {
-    if (some > 0) {
-      const Pack<float, 4> hp = load_pack<float, 4>(st), rp = load_pack<float, 4>(ap);
-      const Pack<T, 4> b4 = load_pack<T, 4>(bp), c4 = load_pack<T, 4>(cp);
+  const int n1 = some > 0 ? n0 : 0;  // lanes behind the last entry read the first, for nothing
+  const int64_t gn1 = gn - n0 + n1;
+  // every load of the lane, none of them conditional and none of them looked at before the last is issued
+  Pack<float, VEC ? 4 : 1> hp[ROWS][VEC ? 1 : 4], ap[VEC ? 1 : 4];
+  Pack<T, VEC ? 4 : 1> bp[ROWS][VEC ? 1 : 4], cp[ROWS][VEC ? 1 : 4];
+  Pack<T, 1> x[ROWS], dt[ROWS], z[ROWS];
+  const bool gate = a.z.p != nullptr;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = hp.get(k), A[k] = rp.get(k), bv[k] = b4.get(k), cv[k] = c4.get(k);
+  for (int m = 0; m < ROWS; ++m) {
+    const int64_t b = b0 + m < B ? b0 + m : B - 1;
+#pragma unroll
+    for (int k = 0; k < (VEC ? 1 : 4); ++k) {
+      const int e = k < some ? k : 0;
+      hp[m][k] = load_pack<float, VEC ? 4 : 1>(state + (b * a.C + c) * a.N + n1 + e);
+      bp[m][k] = load_pack<T, VEC ? 4 : 1>(a.bm.row(b, 0) + gn1 + e);
+      cp[m][k] = load_pack<T, VEC ? 4 : 1>(a.cm.row(b, 0) + gn1 + e);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < some) h[k] = st[k], A[k] = ap[k], bv[k] = to_f32(bp[k]), cv[k] = to_f32(cp[k]);
+    x[m] = load_pack<T, 1>(a.x.row(b, 0) + c);
+    dt[m] = load_pack<T, 1>(a.dt.row(b, 0) + c);
+    z[m] = load_pack<T, 1>((gate ? a.z : a.x).row(b, 0) + c);
   }
-  const float x = to_f32(a.x.row(b, 0)[c]);
-  float s = to_f32(a.dt.row(b, 0)[c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-  const float z = a.z.p ? to_f32(a.z.row(b, 0)[c]) : 0.f;
-  if (a.softplus) s = softplus(s);
-  const float sx = s * x;
-  float y = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    h[k] = fmaf(ex2(s * (A[k] * LOG2E)), h[k], sx * bv[k]);
-    y = fmaf(cv[k], h[k], y);
-  }
-  for (int off = 1; off < lpc; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-  if (!on) return;
-  if (VEC) {
-    if (some > 0) store_pack<float, 4>(st, to_pack<float, 4>(h));
-  } else {
+  for (int k = 0; k < (VEC ? 1 : 4); ++k)
+    ap[k] = load_pack<float, VEC ? 4 : 1>(a.A + (int64_t)c * a.N + n1 + (k < some ? k : 0));
+  const float D = a.D ? a.D[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < some) st[k] = h[k];
-  }
-  if (q == 0) {
-    y = fmaf(a.D ? a.D[c] : 0.f, x, y);
-    if (a.z.p) y *= silu(z);
-    a.y.row(b, 0)[c] = from_f32<T>(y);
+  for (int m = 0; m < ROWS; ++m) {
+    float step = dt[m].get(0) + bias;
+    if (a.softplus) step = softplus(step);
+    const float xv = x[m].get(0), sx = step * xv;
+    float h[4], y = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = VEC ? 0 : k, e = VEC ? k : 0;
+      h[k] = fmaf(ex2(step * (ap[i].get(e) * LOG2E)), hp[m][i].get(e), sx * bp[m][i].get(e));
+      if (k < some) y = fmaf(cp[m][i].get(e), h[k], y);
+    }
+    for (int off = 1; off < lpc; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    if (on && b0 + m < B) {
+      float* st = state + ((b0 + m) * a.C + c) * a.N + n0;
+      if (VEC) {
+        if (some > 0) store_pack<float, 4>(st, to_pack<float, 4>(h));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < some) st[k] = h[k];
+      }
+      if (q == 0) {
+        y = fmaf(D, xv, y);
+        if (gate) y *= silu(z[m].get(0));
+        a.y.row(b0 + m, 0)[c] = from_f32<T>(y);
+      }
+    }
   }
 }
 
+template <typename T, bool VEC>
+cudaError_t launch_token_as(Args<T> a, float* state, int64_t B, int lpc, cudaStream_t st) {
+  // four sequences a lane where that still makes eight blocks for every SM
+  if (ceil_div(B, 4) * a.C * lpc >= int64_t(148) * 8 * LANES) {
+    a.total = (uint32_t)(ceil_div(B, 4) * a.C);
+    k_selective_step<T, VEC, 4><<<(unsigned)ceil_div((int64_t)a.total * lpc, LANES), LANES, 0, st>>>(a, state, B, lpc);
+  } else {
+    a.total = (uint32_t)(B * a.C);
+    k_selective_step<T, VEC, 1><<<(unsigned)ceil_div((int64_t)a.total * lpc, LANES), LANES, 0, st>>>(a, state, B, lpc);
+  }
+  return cudaGetLastError();
+}
+
 template <typename T>
-cudaError_t launch_token(Args<T> a, float* state, int64_t B, cudaStream_t st) {
+cudaError_t launch_token(const Args<T>& a, float* state, int64_t B, cudaStream_t st) {
   int lpc = 1;
   while (lpc * 4 < a.N) lpc *= 2;
-  a.total = (uint32_t)(B * a.C);
-  const unsigned blocks = (unsigned)ceil_div((int64_t)a.total * lpc, LANES);
-  const uintptr_t f = reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(a.A);
-  const uintptr_t t = reinterpret_cast<uintptr_t>(a.bm.p) | reinterpret_cast<uintptr_t>(a.cm.p) | a.bm.bs * sizeof(T);
+  const uintptr_t t = reinterpret_cast<uintptr_t>(a.bm.p) | reinterpret_cast<uintptr_t>(a.cm.p) |
+                      (uintptr_t)(B > 1 ? a.bm.bs * sizeof(T) : 0);
   // four entries by one access: whole fours of states, on 16 bytes (B and C: on four elements)
-  if (a.N % 4 == 0 && (f & 15) == 0 && (t & (4 * sizeof(T) - 1)) == 0)
-    k_selective_step<T, true><<<blocks, LANES, 0, st>>>(a, state, lpc);
-  else
-    k_selective_step<T, false><<<blocks, LANES, 0, st>>>(a, state, lpc);
-  return cudaGetLastError();
+  if (a.N % 4 == 0 && on_16(state) && on_16(a.A) && (t & (4 * sizeof(T) - 1)) == 0)
+    return launch_token_as<T, true>(a, state, B, lpc, st);
+  return launch_token_as<T, false>(a, state, B, lpc, st);
 }
 
 ssd_status validate(const ssd_selective_dims* d, int64_t seqlen) {

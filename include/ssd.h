@@ -499,7 +499,7 @@ ssd_status ssd_selective_step(const ssd_selective_dims* d, const void* x, int64_
                               const float* D, const void* z, int64_t z_bstride, const float* dt_bias, float* state,
                               void* y, int64_t y_bstride, void* stream);
 
-/* batch, seqlen, features >= 1; ngroups >= 1 dividing features. */
+/* batch, seqlen, features >= 1; ngroups >= 1 dividing features, at most 65535; B*L < 2^31 (else SSD_ERR_UNSUPPORTED). */
 typedef struct ssd_norm_dims {
   int64_t batch;    /* B */
   int64_t seqlen;   /* L */
