@@ -15,7 +15,6 @@ namespace ssd {
 namespace conv {
 
 constexpr int THREADS = 128;
-constexpr int AHEAD = 4;  // rows that a thread loads before it computes the AHEAD before them
 
 template <typename T>
 struct Args {
@@ -28,7 +27,7 @@ struct Args {
   const int32_t* lengths;
   int64_t B, L, C;
   uint32_t nvec, ntiles, total;
-  int tile;  // tokens per thread, a multiple of AHEAD
+  int tile;  // tokens per thread, at least W - 1
 };
 
 template <int W, int VEC, bool SILU>
@@ -70,8 +69,9 @@ struct Taps {
   }
 };
 
-template <typename T, int W, int VEC, bool SILU>
-__global__ void __launch_bounds__(THREADS, 4) k_conv_fwd(const Args<T> a) {
+// AHEAD: rows that a thread loads before it computes the AHEAD rows before them
+template <typename T, int W, int VEC, bool SILU, int AHEAD>
+__global__ void __launch_bounds__(THREADS, AHEAD == 8 ? 3 : 4) k_conv_fwd(const Args<T> a) {
   const uint32_t idx = blockIdx.x * THREADS + threadIdx.x;
   if (idx >= a.total) return;
   const uint32_t r = idx / a.nvec;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, 
 // before a run are read twice, so longer runs read less), at most 64.
 inline int tile_tokens(int64_t B, int64_t L, int64_t nvec) {
   int tile = 64;
-  while (tile > AHEAD && B * nvec * ceil_div(L, tile) < 148 * 1024) tile /= 2;
+  while (tile > 8 && B * nvec * ceil_div(L, tile) < 148 * 1024) tile /= 2;
   return tile;
 }
 
@@ -205,10 +205,19 @@ cudaError_t launch(const Args<T>& a0, bool use_silu, cudaStream_t st) {
   a.ntiles = (uint32_t)ceil_div(a.L, tile);
   a.total = (uint32_t)(a.B * nvec * a.ntiles);
   const unsigned blocks = (a.total + THREADS - 1) / THREADS;
+  // Eight rows ahead keep HBM busy at three blocks per SM (131072 tokens x 5376 channels bf16 481 us, 520 with four
+  // rows and four blocks); short runs are over before that pays (5 x 1111 tokens x 1792 channels f32 6.3 us with four
+  // rows, 7.3 with eight).
+  auto go = [&](auto silu) {
+    if (tile >= 32)
+      k_conv_fwd<T, W, VEC, silu.value, 8><<<blocks, THREADS, 0, st>>>(a);
+    else
+      k_conv_fwd<T, W, VEC, silu.value, 4><<<blocks, THREADS, 0, st>>>(a);
+  };
   if (use_silu)
-    k_conv_fwd<T, W, VEC, true><<<blocks, THREADS, 0, st>>>(a);
+    go(std::true_type());
   else
-    k_conv_fwd<T, W, VEC, false><<<blocks, THREADS, 0, st>>>(a);
+    go(std::false_type());
   return cudaGetLastError();
 }
 

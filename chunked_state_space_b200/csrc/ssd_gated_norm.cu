@@ -24,10 +24,37 @@ struct Args {
   int64_t n;  // features of a group
 };
 
+// u of a piece, and the sum of its squares
 template <typename T, int VEC>
-__device__ __forceinline__ void gated(const Pack<T, VEC>& x, const Pack<T, VEC>& z, bool gate, float (&u)[VEC]) {
+__device__ __forceinline__ float gated(const Pack<T, VEC>& x, const Pack<T, VEC>& z, bool gate, float (&u)[VEC]) {
+  if constexpr (VEC == 1) {
+    u[0] = gate ? x.get(0) * silu(z.get(0)) : x.get(0);
+    return u[0] * u[0];
+  } else {
+    F2 ss = both(0.f);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) u[i] = gate ? x.get(i) * silu(z.get(i)) : x.get(i);
+    for (int i = 0; i < VEC; i += 2) {
+      F2 v{x.get(i), x.get(i + 1)};
+      if (gate) v = mul2(v, silu2(F2{z.get(i), z.get(i + 1)}));
+      ss = fma2(v, v, ss);
+      u[i] = v.x, u[i + 1] = v.y;
+    }
+    return ss.x + ss.y;
+  }
+}
+
+// u times inv and the weights
+template <int VEC>
+__device__ __forceinline__ void scaled(float (&u)[VEC], float inv, const float (&w)[VEC]) {
+  if constexpr (VEC == 1) {
+    u[0] *= inv * w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const F2 v = mul2(mul2(F2{u[i], u[i + 1]}, both(inv)), F2{w[i], w[i + 1]});
+      u[i] = v.x, u[i + 1] = v.y;
+    }
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -72,11 +99,7 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      if (me + k * all < pieces) {
-        gated(x[k], z[k], gate, u[k]);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ss = fmaf(u[k][i], u[k][i], ss);
-      }
+      if (me + k * all < pieces) ss += gated(x[k], z[k], gate, u[k]);
     }
     if (row + step < a.rows) fetch(row + step);
     ss = warp_sum(ss);
@@ -94,10 +117,8 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
     for (int k = 0; k < PER; ++k) {
       const int p = me + k * all;
       if (p < pieces) {
-        float o[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = u[k][i] * inv * w[k][i];
-        store_pack<T, VEC>(out + (int64_t)p * VEC, to_pack<T, VEC>(o));
+        scaled(u[k], inv, w[k]);
+        store_pack<T, VEC>(out + (int64_t)p * VEC, to_pack<T, VEC>(u[k]));
       }
     }
   }
@@ -115,9 +136,7 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
   const int64_t pieces = a.n / VEC;
   float u[VEC], ss = 0.f;
   for (int64_t p = threadIdx.x; p < pieces; p += MOST) {
-    gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) ss = fmaf(u[i], u[i], ss);
+    ss += gated(load_pack<T, VEC>(x + p * VEC), load_pack<T, VEC>(z + p * VEC), gate, u);
   }
   ss = warp_sum(ss);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
@@ -131,8 +150,7 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = 1.f;
     if (a.weight) load_params<VEC, (VEC > 1)>(a.weight + g0 + p * VEC, w);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) u[i] *= inv * w[i];
+    scaled(u, inv, w);
     store_pack<T, VEC>(out + p * VEC, to_pack<T, VEC>(u));
   }
 }
