@@ -3,15 +3,14 @@
 // Bound by HBM: x and z are read once and out is written once.  A run of
 // features (one group of one row) is held in registers as u between the sum
 // and the scaling, PER 16-byte pieces per thread; blocks stay for many rows,
-// with their weights in registers and the next row's loads under way while
-// this one's sum is reduced.  The sum of squares is f32, in a fixed order.
+// with the next row's loads under way while this one's sum is reduced.  The sum of squares is f32, in a fixed order.
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace gnorm {
 
-constexpr int PER = 4;  // pieces of a row per thread
-constexpr int MOST = 512;  // threads of a block
+constexpr int PER = 5;     // pieces of a row per thread
+constexpr int MOST = 640;  // threads of a block (which leaves a thread 96 registers)
 
 template <typename T>
 struct Args {
@@ -74,12 +73,17 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
   const bool gate = a.z.p != nullptr;
   int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   const int64_t step = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
-  float w[PER][VEC];
+  // A warp with a run of its own holds the weights; a block reads them again for each row (from L1): their registers
+  // would cost it a quarter of its warps (16384 rows of 5120 features bf16: 97 us, against 82).
+  auto weights = [&](int k, float (&w)[VEC]) {
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
+    for (int i = 0; i < VEC; ++i) w[i] = 1.f;
+    if (a.weight && me + k * all < pieces) load_params<VEC, (VEC > 1)>(a.weight + g0 + (int64_t)(me + k * all) * VEC, w);
+  };
+  float held[BLOCK ? 1 : PER][VEC];
+  if constexpr (!BLOCK) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[k][i] = 1.f;
-    if (a.weight && me + k * all < pieces) load_params<VEC, (VEC > 1)>(a.weight + g0 + (int64_t)(me + k * all) * VEC, w[k]);
+    for (int k = 0; k < PER; ++k) weights(k, held[k]);
   }
   Pack<T, VEC> x[PER], z[PER];
   auto fetch = [&](int64_t r) {
@@ -117,7 +121,8 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
     for (int k = 0; k < PER; ++k) {
       const int p = me + k * all;
       if (p < pieces) {
-        scaled(u[k], inv, w[k]);
+        if constexpr (BLOCK) weights(k, held[0]);
+        scaled(u[k], inv, held[BLOCK ? 0 : k]);
         store_pack<T, VEC>(out + (int64_t)p * VEC, to_pack<T, VEC>(u[k]));
       }
     }
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
 }
 
 // A run of up to 32 * PER pieces takes a warp, a longer one a block of as many
-// warps as hold it; the grid is what the SMs hold at 128 registers a thread.
+// warps as hold it; the grid is what the SMs hold at 96 registers a thread.
 template <typename T, int VEC>
 cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
   const int64_t pieces = a.n / VEC;
@@ -165,7 +170,7 @@ cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
     k_gated_norm<T, VEC, false><<<dim3(blocks(ceil_div(a.rows, 4), 148 * 4), groups), 128, 0, st>>>(a);
   } else if (pieces <= MOST * PER) {
     const int64_t threads = ceil_div(ceil_div(pieces, PER), 32) * 32;
-    k_gated_norm<T, VEC, true><<<dim3(blocks(a.rows, 148 * (512 / threads)), groups), (unsigned)threads, 0, st>>>(a);
+    k_gated_norm<T, VEC, true><<<dim3(blocks(a.rows, 148 * (MOST / threads)), groups), (unsigned)threads, 0, st>>>(a);
   } else {
     k_gated_norm_long<T, VEC><<<dim3((unsigned)a.rows, groups), MOST, 0, st>>>(a);
   }
