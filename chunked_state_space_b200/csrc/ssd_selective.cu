@@ -69,8 +69,11 @@ struct Shape {
   // memory, or in registers as single elements)
   static constexpr int TT = NP <= 16 ? 8 * HELPERS / CB : NP == 32 ? (BVEC ? 32 : 16) : NP == 64 ? (BVEC ? 16 : 8) : 8;
   static constexpr int XP = TT * CB / V, BP = TT * NP / VB;        // pieces of a tile of x (dt, z), of B (C)
+  // B and C of an entry lie side by side: two bf16 in a word (half the shared-memory traffic, which would bound the
+  // kernel, for two instructions more per entry), or two f32
+  static constexpr int WORDS = sizeof(T) == 2 ? 1 : 2;
   static constexpr int NX = (XP + HELPERS - 1) / HELPERS;          // of them, per helper thread
-  static constexpr int NB = (2 * BP + HELPERS - 1) / HELPERS;      // (of B and C together)
+  static constexpr int NB = (BP + HELPERS - 1) / HELPERS;
   // y's sums over the states are left in PW parts per (token, channel), which the output pass adds up; more lanes than
   // that exchange theirs first, RED tokens together, each exchange halving what a lane still holds.
   static constexpr int PW = LPC < 4 ? LPC : 4, RED = LPC / PW;
@@ -107,9 +110,9 @@ template <typename T, int NS, int LPC, bool VEC, bool BVEC>
 __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective(const Args<T> a) {
   using S = Shape<T, NS, LPC, VEC, BVEC>;
   constexpr int CB = S::CB, NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
-                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS;
+                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS, WORDS = S::WORDS;
   __shared__ __align__(16) float2 s_step[2][ROWS * CB];    // (s, s x)
-  __shared__ __align__(16) float s_bc[2][2][ROWS * NP];    // B, C
+  __shared__ __align__(16) uint32_t s_bc[2][ROWS * NP * WORDS];  // (B, C)
   __shared__ __align__(16) float s_y[2][TT * CB * PW];
   __shared__ __align__(16) float s_D[CB], s_bias[CB];
   const uint32_t r = blockIdx.x / a.blocks_per_group, cb = blockIdx.x - r * a.blocks_per_group;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
     // ---- operands: the step and the scaled input of every (token, channel), B and C
     const int me = tid - LANES;
     Pack<T, V> nx[NX], nd[NX];
-    Pack<T, VB> nb[NB];
+    Pack<T, VB> nb[NB], nc2[NB];
     auto fetch = [&](int64_t t0) {
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
@@ -204,9 +207,11 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        const int ii = me + k * HELPERS, i = ii < BP ? ii : ii - BP, t = i / (NP / VB), n = i % (NP / VB) * VB;
-        if (ii < 2 * BP && t0 + t < len && n < a.N)
-          nb[k] = load_pack<T, VB>((ii < BP ? a.bm : a.cm).row(b, t0 + t) + (int64_t)g * a.N + n);
+        const int i = me + k * HELPERS, t = i / (NP / VB), n = i % (NP / VB) * VB;
+        if (i < BP && t0 + t < len && n < a.N) {
+          nb[k] = load_pack<T, VB>(a.bm.row(b, t0 + t) + (int64_t)g * a.N + n);
+          nc2[k] = load_pack<T, VB>(a.cm.row(b, t0 + t) + (int64_t)g * a.N + n);
+        }
       }
     };
     fetch(0);
@@ -245,12 +250,26 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        const int ii = me + k * HELPERS, i = ii < BP ? ii : ii - BP, t = i / (NP / VB), n = i % (NP / VB) * VB;
-        if (ii < 2 * BP) {
+        const int i = me + k * HELPERS, t = i / (NP / VB), n = i % (NP / VB) * VB;
+        if (i < BP) {
           const bool in = t0 + t < len && n < a.N;
-          float* to = &s_bc[k2][ii < BP ? 0 : 1][i * VB];
+          uint32_t w[VB * WORDS];
 #pragma unroll
-          for (int e = 0; e < VB; ++e) to[e] = in ? nb[k].get(e) : 0.f;
+          for (int e = 0; e < VB; ++e) {
+            const uint32_t bw = in ? __float_as_uint(nb[k].get(e)) : 0u, cw = in ? __float_as_uint(nc2[k].get(e)) : 0u;
+            if constexpr (WORDS == 1)
+              w[e] = __byte_perm(bw, cw, 0x7632);
+            else
+              w[2 * e] = bw, w[2 * e + 1] = cw;
+          }
+          uint32_t* to = &s_bc[k2][i * VB * WORDS];
+          if constexpr (VB * WORDS % 4 == 0) {
+#pragma unroll
+            for (int e = 0; e < VB * WORDS; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VB * WORDS; ++e) to[e] = w[e];
+          }
         }
       }
       arrive_at(FULL + k2);
@@ -272,26 +291,28 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
   }
   struct Operands {  // of U tokens
     float2 st[U];
-    float b[U][NS], c[U][NS];
+    uint32_t bc[U][NS * WORDS];
+    __device__ __forceinline__ float b(int j, int k) const {
+      return __uint_as_float(WORDS == 1 ? bc[j][k] << 16 : bc[j][2 * k]);
+    }
+    __device__ __forceinline__ float c(int j, int k) const {
+      return __uint_as_float(WORDS == 1 ? bc[j][k] & 0xffff0000u : bc[j][(2 * k + 1) % (NS * WORDS)]);
+    }
   };
   auto read = [&](int k2, int tg, Operands& o) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int t = tg + j;
       o.st[j] = s_step[k2][S::at(t, ch)];
-      const float* bt = &s_bc[k2][0][t * NP + q * NS];
-      const float* ct = &s_bc[k2][1][t * NP + q * NS];
-      if constexpr (NS % 4 == 0) {
+      const uint32_t* from = &s_bc[k2][(t * NP + q * NS) * WORDS];
+      if constexpr (NS * WORDS % 4 == 0) {
 #pragma unroll
-        for (int k = 0; k < NS; k += 4) {
-          *reinterpret_cast<float4*>(&o.b[j][k]) = *reinterpret_cast<const float4*>(bt + k);
-          *reinterpret_cast<float4*>(&o.c[j][k]) = *reinterpret_cast<const float4*>(ct + k);
-        }
-      } else if constexpr (NS == 2) {
-        *reinterpret_cast<float2*>(o.b[j]) = *reinterpret_cast<const float2*>(bt);
-        *reinterpret_cast<float2*>(o.c[j]) = *reinterpret_cast<const float2*>(ct);
+        for (int k = 0; k < NS * WORDS; k += 4)
+          *reinterpret_cast<uint4*>(&o.bc[j][k]) = *reinterpret_cast<const uint4*>(from + k);
+      } else if constexpr (NS * WORDS == 2) {
+        *reinterpret_cast<uint2*>(o.bc[j]) = *reinterpret_cast<const uint2*>(from);
       } else {
-        o.b[j][0] = bt[0], o.c[j][0] = ct[0];
+        o.bc[j][0] = from[0];
       }
     }
   };
@@ -322,17 +343,17 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if constexpr (NS == 1) {
-        h[0] = fmaf(e[j][0], h[0], o.st[j].y * o.b[j][0]);
-        part[j] = o.c[j][0] * h[0];
+        h[0] = fmaf(e[j][0], h[0], o.st[j].y * o.b(j, 0));
+        part[j] = o.c(j, 0) * h[0];
       } else {
         F2 y{0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NS; k += 2) {
-          const F2 bx = mul2(both(o.st[j].y), F2{o.b[j][k], o.b[j][k + 1]});
+          const F2 bx = mul2(both(o.st[j].y), F2{o.b(j, k), o.b(j, k + 1)});
           const F2 hn = fma2(F2{e[j][k], e[j][k + 1]}, F2{h[k], h[k + 1]}, bx);
           h[k] = hn.x;
           h[k + 1] = hn.y;
-          const F2 cv{o.c[j][k], o.c[j][k + 1]};
+          const F2 cv{o.c(j, k), o.c(j, k + 1)};
           y = k == 0 ? mul2(cv, hn) : fma2(cv, hn, y);
         }
         part[j] = y.x + y.y;
