@@ -14,6 +14,8 @@
 // group.  Its inputs come tile by tile: the next tile's rows are loaded into
 // registers while this one is computed; step and scaled input are formed once
 // per (token, channel) and put in shared memory; B and C are widened to f32 once per tile.
+#include <limits.h>
+
 #include "ssd_rows.cuh"
 
 namespace ssd {
@@ -69,6 +71,7 @@ struct Shape {
   // memory, or in registers as single elements)
   static constexpr int TT = NP <= 16 ? 8 * HELPERS / CB : NP == 32 ? (BVEC ? 32 : 16) : NP == 64 ? (BVEC ? 16 : 8) : 8;
   static constexpr int XP = TT * CB / V, BP = TT * NP / VB;        // pieces of a tile of x (dt, z), of B (C)
+  static constexpr int APART = HELPERS / (CB / V);                 // tokens between the pieces of a thread
   // B and C of an entry lie side by side: two bf16 in a word (half the shared-memory traffic, which would bound the
   // kernel, for two instructions more per entry), or two f32
   static constexpr int WORDS = sizeof(T) == 2 ? 1 : 2;
@@ -80,7 +83,7 @@ struct Shape {
   static constexpr int U = RED < 2 ? 2 : RED;  // tokens that a lane works on together
   static constexpr int ROWS = TT + 2 * U;      // rows of operands: a tile, and what the loop reads behind it for nothing
   static_assert(TT % (2 * U) == 0, "a tile is a whole number of turns of its loop");
-  static_assert(NP % VB == 0 && CB % V == 0, "rows of a tile are whole pieces");
+  static_assert(NP % VB == 0 && CB % V == 0 && HELPERS % (CB / V) == 0, "rows of a tile are whole pieces");
   // Where (token, channel) lies in a tile of 8-byte entries: a thread writes V neighbouring channels, two per
   // instruction, so its pairs are turned by the piece's number to fall on different banks; the channels that a warp
   // reads together share the turn or lie in different pieces.
@@ -110,7 +113,7 @@ template <typename T, int NS, int LPC, bool VEC, bool BVEC>
 __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective(const Args<T> a) {
   using S = Shape<T, NS, LPC, VEC, BVEC>;
   constexpr int CB = S::CB, NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
-                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS, WORDS = S::WORDS;
+                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS, WORDS = S::WORDS, APART = S::APART;
   __shared__ __align__(16) float2 s_step[2][ROWS * CB];    // (s, s x)
   __shared__ __align__(16) uint32_t s_bc[2][ROWS * NP * WORDS];  // (B, C)
   __shared__ __align__(16) float s_y[2][TT * CB * PW];
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
   const int nc = min(CB, ((int)g + 1) * a.per_group - c0);
   const int tid = threadIdx.x;
   const int64_t len = row_length(a.lengths, b, a.L);
-  const int64_t tiles = (len + TT - 1) / TT;
+  const int tiles = (int)((len + TT - 1) / TT);
   for (int i = tid; i < CB; i += THREADS) {
     s_D[i] = a.D && i < nc ? a.D[c0 + i] : 0.f;
     s_bias[i] = a.dt_bias && i < nc ? a.dt_bias[c0 + i] : 0.f;
@@ -133,59 +136,67 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
     const int me = tid - LANES - HELPERS;
     const bool gate = a.z.p != nullptr;
     for (int k = 0; k < 2 && k < tiles; ++k) arrive_at(FULL + k);
+    // piece k of a thread: token t0 + k * APART of the tile, channels c ..
+    const int t0 = me / (CB / V), c = me % (CB / V) * V;
+    const T* px = a.x.row(b, t0) + c0 + c;
+    const T* pz = gate ? a.z.row(b, t0) + c0 + c : px;
+    T* py = a.y.row(b, t0) + c0 + c;
     Pack<T, V> nx[NX], nz[NX];
-    auto fetch = [&](int64_t t0) {
+    auto fetch = [&](int left) {  // tokens of the sequence from this tile on
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
-        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
-        if (i < XP && t0 + t < len && c < nc) {
-          nx[k] = load_pack<T, V>(a.x.row(b, t0 + t) + c0 + c);
-          if (gate) nz[k] = load_pack<T, V>(a.z.row(b, t0 + t) + c0 + c);
+        if (me + k * HELPERS < XP && t0 + k * APART < left && c < nc) {
+          nx[k] = load_pack<T, V>(px + k * APART * a.x.ts);
+          if (gate) nz[k] = load_pack<T, V>(pz + k * APART * a.z.ts);
         }
       }
+      px += TT * a.x.ts;
+      pz += TT * a.z.ts;
     };
-    fetch(0);
+    int left = (int)min(len, (int64_t)INT_MAX);
+    fetch(left);
 #pragma unroll 1
-    for (int64_t tile = 0; tile < tiles; ++tile) {
-      const int64_t t0 = tile * TT;
-      const int k2 = (int)(tile & 1);
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int k2 = tile & 1;
       Pack<T, V> x[NX], z[NX];
 #pragma unroll
       for (int k = 0; k < NX; ++k) x[k] = nx[k], z[k] = nz[k];
-      if (tile + 1 < tiles) fetch(t0 + TT);
+      if (tile + 1 < tiles) fetch(left - TT);
       wait_for(DONE + k2);
-      auto sum = [&](int t, int c) {
-        const float* p = &s_y[k2][S::sum_at(t, c)];
+      // sums of channels c + e and, where two are asked for, c + e + 1
+      auto sums = [&](int t, int e) {
+        const float* p = &s_y[k2][S::sum_at(t, c + e)];
+        const float* r = &s_y[k2][S::sum_at(t, V > 1 ? c + e + 1 : c + e)];
         if constexpr (PW == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p);
-          return (v.x + v.y) + (v.z + v.w);
-        } else if constexpr (PW == 2) {
-          const float2 v = *reinterpret_cast<const float2*>(p);
-          return v.x + v.y;
+          const float4 v = *reinterpret_cast<const float4*>(p), w = *reinterpret_cast<const float4*>(r);
+          const F2 f = add2(F2{v.x, v.y}, F2{v.z, v.w}), g = add2(F2{w.x, w.y}, F2{w.z, w.w});
+          return F2{f.x + f.y, g.x + g.y};
         } else {
-          return p[0];
+          const float2 v = *reinterpret_cast<const float2*>(p), w = *reinterpret_cast<const float2*>(r);
+          return F2{v.x + v.y, w.x + w.y};
         }
       };
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
-        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
-        if (i < XP && t0 + t < len && c < nc) {
+        const int t = t0 + k * APART;
+        if (me + k * HELPERS < XP && t < left && c < nc) {
           float out[V];
           if constexpr (V == 1) {
-            out[0] = fmaf(s_D[c], x[k].get(0), sum(t, c));
+            out[0] = fmaf(s_D[c], x[k].get(0), sums(t, 0).x);
             if (gate) out[0] *= silu(z[k].get(0));
           } else {
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-              F2 y = fma2(F2{s_D[c + e], s_D[c + e + 1]}, F2{x[k].get(e), x[k].get(e + 1)},
-                          F2{sum(t, c + e), sum(t, c + e + 1)});
+              F2 y = fma2(F2{s_D[c + e], s_D[c + e + 1]}, F2{x[k].get(e), x[k].get(e + 1)}, sums(t, e));
               if (gate) y = mul2(y, silu2(F2{z[k].get(e), z[k].get(e + 1)}));
               out[e] = y.x, out[e + 1] = y.y;
             }
           }
-          store_pack<T, V>(a.y.row(b, t0 + t) + c0 + c, to_pack<T, V>(out));
+          store_pack<T, V>(py + k * APART * a.y.ts, to_pack<T, V>(out));
         }
       }
+      py += TT * a.y.ts;
+      left -= TT;
       if (tile + 2 < tiles) arrive_at(FULL + k2);
     }
     return;
@@ -194,38 +205,46 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
   if (tid >= LANES) {
     // ---- operands: the step and the scaled input of every (token, channel), B and C
     const int me = tid - LANES;
+    const int t0 = me / (CB / V), c = me % (CB / V) * V;
+    const T* px = a.x.row(b, t0) + c0 + c;
+    const T* pd = a.dt.row(b, t0) + c0 + c;
+    const T* pb = a.bm.row(b, 0) + (int64_t)g * a.N;
+    const T* pc = a.cm.row(b, 0) + (int64_t)g * a.N;
     Pack<T, V> nx[NX], nd[NX];
     Pack<T, VB> nb[NB], nc2[NB];
-    auto fetch = [&](int64_t t0) {
+    auto fetch = [&](int left) {
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
-        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
-        if (i < XP && t0 + t < len && c < nc) {
-          nx[k] = load_pack<T, V>(a.x.row(b, t0 + t) + c0 + c);
-          nd[k] = load_pack<T, V>(a.dt.row(b, t0 + t) + c0 + c);
+        if (me + k * HELPERS < XP && t0 + k * APART < left && c < nc) {
+          nx[k] = load_pack<T, V>(px + k * APART * a.x.ts);
+          nd[k] = load_pack<T, V>(pd + k * APART * a.dt.ts);
         }
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const int i = me + k * HELPERS, t = i / (NP / VB), n = i % (NP / VB) * VB;
-        if (i < BP && t0 + t < len && n < a.N) {
-          nb[k] = load_pack<T, VB>(a.bm.row(b, t0 + t) + (int64_t)g * a.N + n);
-          nc2[k] = load_pack<T, VB>(a.cm.row(b, t0 + t) + (int64_t)g * a.N + n);
+        if (i < BP && t < left && n < a.N) {
+          nb[k] = load_pack<T, VB>(pb + t * a.bm.ts + n);
+          nc2[k] = load_pack<T, VB>(pc + t * a.cm.ts + n);
         }
       }
+      px += TT * a.x.ts;
+      pd += TT * a.dt.ts;
+      pb += TT * a.bm.ts;
+      pc += TT * a.cm.ts;
     };
-    fetch(0);
+    int left = (int)min(len, (int64_t)INT_MAX);
+    fetch(left);
 #pragma unroll 1
-    for (int64_t tile = 0; tile < tiles; ++tile) {
-      const int64_t t0 = tile * TT;
-      const int k2 = (int)(tile & 1);
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int k2 = tile & 1;
       if (tile >= 2) wait_for(DONE + k2);
       // behind the sequence's end the step is 0, which leaves the state as it is
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
-        const int i = me + k * HELPERS, t = i / (CB / V), c = i % (CB / V) * V;
-        if (i < XP) {
-          const bool in = t0 + t < len && c < nc;
+        const int t = t0 + k * APART;
+        if (me + k * HELPERS < XP) {
+          const bool in = t < left && c < nc;
           if constexpr (V == 1) {
             float s = 0.f, sx = 0.f;
             if (in) {
@@ -235,16 +254,25 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
             }
             s_step[k2][S::at(t, c)] = make_float2(s, sx);
           } else {
+            F2 s[V / 2], sx[V / 2];
+            if (in) {
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              F2 s = both(0.f), sx = both(0.f);
-              if (in) {
-                s = add2(F2{nd[k].get(e), nd[k].get(e + 1)}, F2{s_bias[c + e], s_bias[c + e + 1]});
-                if (a.softplus) s = softplus2(s);
-                sx = mul2(s, F2{nx[k].get(e), nx[k].get(e + 1)});
+              for (int e = 0; e < V; e += 2)
+                s[e / 2] = add2(F2{nd[k].get(e), nd[k].get(e + 1)}, F2{s_bias[c + e], s_bias[c + e + 1]});
+              if (a.softplus) {
+#pragma unroll
+                for (int e = 0; e < V; e += 2) s[e / 2] = softplus2(s[e / 2]);
               }
-              *reinterpret_cast<float4*>(&s_step[k2][S::at(t, c + e)]) = make_float4(s.x, sx.x, s.y, sx.y);
+#pragma unroll
+              for (int e = 0; e < V; e += 2) sx[e / 2] = mul2(s[e / 2], F2{nx[k].get(e), nx[k].get(e + 1)});
+            } else {
+#pragma unroll
+              for (int e = 0; e < V; e += 2) s[e / 2] = sx[e / 2] = both(0.f);
             }
+#pragma unroll
+            for (int e = 0; e < V; e += 2)
+              *reinterpret_cast<float4*>(&s_step[k2][S::at(t, c + e)]) =
+                  make_float4(s[e / 2].x, sx[e / 2].x, s[e / 2].y, sx[e / 2].y);
           }
         }
       }
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
       for (int k = 0; k < NB; ++k) {
         const int i = me + k * HELPERS, t = i / (NP / VB), n = i % (NP / VB) * VB;
         if (i < BP) {
-          const bool in = t0 + t < len && n < a.N;
+          const bool in = t < left && n < a.N;
           uint32_t w[VB * WORDS];
 #pragma unroll
           for (int e = 0; e < VB; ++e) {
@@ -265,17 +293,19 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
           uint32_t* to = &s_bc[k2][i * VB * WORDS];
           if constexpr (VB * WORDS % 4 == 0) {
 #pragma unroll
-            for (int e = 0; e < VB * WORDS; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            for (int e = 0; e < VB * WORDS; e += 4)
+              *reinterpret_cast<uint4*>(to + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
           } else {
 #pragma unroll
             for (int e = 0; e < VB * WORDS; ++e) to[e] = w[e];
           }
         }
       }
+      left -= TT;
       arrive_at(FULL + k2);
-      if (tile + 1 < tiles) fetch(t0 + TT);
+      if (tile + 1 < tiles) fetch(left);
     }
-    for (int64_t tile = tiles > 2 ? tiles - 2 : 0; tile < tiles; ++tile) arrive_at(DONE + (int)(tile & 1));
+    for (int tile = tiles > 2 ? tiles - 2 : 0; tile < tiles; ++tile) arrive_at(DONE + (tile & 1));
     return;
   }
 
@@ -378,8 +408,8 @@ __global__ void __launch_bounds__(THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2
     if (!DEFER) store(k2, tg);
   };
 #pragma unroll 1
-  for (int64_t tile = 0; tile < tiles; ++tile) {
-    const int k2 = (int)(tile & 1);
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int k2 = tile & 1;
     wait_for(FULL + k2);
     // Software pipeline over groups of U tokens: while group g is finished, the exponentials of g + 1 are under way
     // and the operands of g + 2 are loaded.
