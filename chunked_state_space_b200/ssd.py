@@ -422,6 +422,13 @@ def ssd_step(x, dt, A, Bm, Cm, state, D=None, y=None, stream=None, input_dt: boo
 # what the call takes (address and strides).
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_IO_CODES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
+def _io(x: torch.Tensor) -> int:
+    code = _IO_CODES.get(x.dtype)
+    return _io_code(x) if code is None else code
 
 
 def _device_of(x: torch.Tensor) -> int:
@@ -444,7 +451,7 @@ def _rows(t: Optional[torch.Tensor], shape, dtype, dev: int, outer: tuple):
     `outer`: what stands for the strides of None."""
     if t is None:
         return (None,) + outer
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _mismatch(t, shape, dtype, dev)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
@@ -456,7 +463,7 @@ def _whole(t: Optional[torch.Tensor], shape, dtype, dev: int):
     """Address of a parameter or state: None or of `shape`, `dtype` and device, contiguous."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _mismatch(t, shape, dtype, dev)
     return t.data_ptr()
 
@@ -486,7 +493,7 @@ def _call(name: str, dev: int, stream, *args):
     else:
         handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     fn = getattr(_lib or lib(), name)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         s = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -521,7 +528,7 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, lengths=None, silu: bool
         y = _new_rows(x, lengths)
     if final_state is None and want_final:
         final_state = torch.empty((Bz, max(W - 1, 0), C), dtype=io, device=x.device)
-    dims = ConvDims(Bz, L, C, W, _io_code(x), int(silu))
+    dims = ConvDims(Bz, L, C, W, _io(x), int(silu))
     _call("ssd_conv_fwd", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE2),
           _whole(weight, (C, W), f32, dev), _whole(bias, (C,), f32, dev), _whole(init_state, (Bz, W - 1, C), io, dev),
           _whole(lengths, (Bz,), torch.int32, dev), *_rows(y, shape, io, dev, _NONE2),
@@ -540,7 +547,7 @@ def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream
     dev, io, f32 = _device_of(x), x.dtype, torch.float32
     if y is None:
         y = _new_rows(x)
-    dims = ConvDims(Bz, 1, C, W, _io_code(x), int(silu))
+    dims = ConvDims(Bz, 1, C, W, _io(x), int(silu))
     _call("ssd_conv_step", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE1),
           _whole(weight, (C, W), f32, dev), _whole(bias, (C,), f32, dev), _whole(state, (Bz, W - 1, C), io, dev),
           *_rows(y, shape, io, dev, _NONE1))
@@ -564,7 +571,7 @@ def ssd_selective_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state
         y = _new_rows(x, lengths)
     if final_state is None and want_final:
         final_state = torch.empty((Bz, C, N), dtype=f32, device=x.device)
-    dims = SelectiveDims(Bz, L, C, N, G, _io_code(x), int(softplus))
+    dims = SelectiveDims(Bz, L, C, N, G, _io(x), int(softplus))
     _call("ssd_selective_fwd", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE2),
           *_rows(dt, shape, io, dev, _NONE2), _whole(A, (C, N), f32, dev), at_b, at_c, *bc, _whole(D, (C,), f32, dev),
           *_rows(z, shape, io, dev, _NONE2), _whole(dt_bias, (C,), f32, dev),
@@ -585,7 +592,7 @@ def ssd_selective_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, so
     G, N, at_b, at_c, bc = _groups(x, Bm, Cm, dev)
     if y is None:
         y = _new_rows(x)
-    dims = SelectiveDims(Bz, 1, C, N, G, _io_code(x), int(softplus))
+    dims = SelectiveDims(Bz, 1, C, N, G, _io(x), int(softplus))
     _call("ssd_selective_step", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE1),
           *_rows(dt, shape, io, dev, _NONE1), _whole(A, (C, N), f32, dev), at_b, at_c, *bc, _whole(D, (C,), f32, dev),
           *_rows(z, shape, io, dev, _NONE1), _whole(dt_bias, (C,), f32, dev), _whole(state, (Bz, C, N), f32, dev),
@@ -607,7 +614,7 @@ def ssd_rmsnorm_gated(x, z=None, weight=None, eps: float = 1e-5, ngroups: int = 
         L, none, last = shape[1], _NONE2, ()
     else:
         L, none, last = 1, _NONE1, _NONE1  # one token per row: its stride is not looked at
-    dims = NormDims(shape[0], L, F, int(ngroups), _io_code(x), 0)
+    dims = NormDims(shape[0], L, F, int(ngroups), _io(x), 0)
     _call("ssd_rmsnorm_gated", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, none), *last,
           *_rows(z, shape, io, dev, none), *last, _whole(weight, (F,), torch.float32, dev), float(eps),
           *_rows(out, shape, io, dev, none), *last)

@@ -166,6 +166,16 @@ def scan_want(d, init, lengths=None, softplus=True):
     (2, 300, 1300, 16, 1, (0, 0), True, True, [300, 177]),
     (20, 66, 2048, 16, 1, (0, 0), True, False, None),
     (3, 64, 24576, 4, 1, (0, 0), True, False, None),
+    # each kernel of the prompt, and each way of loading for it: by the number of channels, aligned and not
+    (5, 70, 1024, 16, 1, (8, 8), True, True, None),
+    (5, 67, 1025, 15, 1, (1, 0), True, True, None),
+    (5, 130, 1024, 16, 2, (8, 1), True, True, [130, 0, 1, 63, 129]),
+    (9, 40, 2048, 12, 4, (0, 0), True, True, None),
+    (9, 33, 1700, 16, 1, (0, 0), False, False, [33, 32, 31, 0, 1, 17, 8, 9, 40]),
+    (5, 70, 1024, 32, 1, (0, 0), True, True, None),
+    (5, 35, 1026, 21, 2, (1, 0), True, True, [35, 0, 8, 16, 34]),
+    (2, 96, 2000, 8, 1, (0, 0), True, True, None),
+    (1, 40, 30, 7, 3, (1, 1), True, True, None),
 ])
 def test_selective_matches_64_bits(io, B, L, C, N, G, pad, gate, init, lengths):
     d = scan_inputs(io, B, L, C, N, G, gate=gate, pad=pad)
@@ -173,7 +183,8 @@ def test_selective_matches_64_bits(io, B, L, C, N, G, pad, gate, init, lengths):
     if lengths is not None:
         for k, n in enumerate(lengths):
             for name in ("x", "dt", "z", "Bm", "Cm"):
-                d[name][k, max(n, 0):] = float("nan")
+                if d[name] is not None:
+                    d[name][k, max(n, 0):] = float("nan")
     y = torch.full((B, L, C), 7.0, dtype=IO[io], device="cuda")
     got, fin = ssd.ssd_selective_fwd(**d, init_state=st, lengths=lens(lengths), y=y)
     want, bound, state, sbound = scan_want(d, st, lengths)
