@@ -8,57 +8,60 @@ namespace selective {
 constexpr int STEP_THREADS = 128;
 
 // One token, bound by its f32 state, which is read and written once: four
-// entries to a lane, a channel on ceil(N / 4) lanes (rounded up to a power of
-// two), y summed by shuffles.  A lane takes its channel of up to ROWS
-// sequences, with A, D and the bias loaded once.
+// entries to a lane, a channel on lpc = ceil(N / 4) lanes (rounded up to a
+// power of two).  The lanes take their channel of ROWS sequences together,
+// with A loaded once: each loads all its entries, but the step, input, gate and
+// output of one sequence only, which the others get from it by shuffles, and
+// the ROWS sums of y are exchanged so that each ends up where its sequence is.
 template <typename T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(STEP_THREADS) k_selective_step(const Args<T> a, float* state, int64_t B, int lpc) {
   const uint32_t i = (blockIdx.x * STEP_THREADS + threadIdx.x) / lpc;
-  const int q = threadIdx.x % lpc;
+  const int lane = threadIdx.x & 31, q = lane & (lpc - 1), first = lane - q;
   const bool on = i < a.total;
   const uint32_t j = on ? i : a.total - 1;  // lanes behind the end take part in the shuffles
   const uint32_t r = j / a.C;
   const int64_t b0 = (int64_t)r * ROWS;
   const int c = (int)(j - r * a.C), n0 = q * 4, some = min(4, a.N - n0);
-  const int64_t gn = (int64_t)(c / a.per_group) * a.N + n0;
   const int n1 = some > 0 ? n0 : 0;  // lanes behind the last entry read the first, for nothing
-  const int64_t gn1 = gn - n0 + n1;
+  const int64_t gn = (int64_t)(c / a.per_group) * a.N + n1;
   // every load of the lane, none of them conditional and none of them looked at before the last is issued
-  Pack<float, VEC ? 4 : 1> hp[ROWS][VEC ? 1 : 4], ap[VEC ? 1 : 4];
-  Pack<T, VEC ? 4 : 1> bp[ROWS][VEC ? 1 : 4], cp[ROWS][VEC ? 1 : 4];
-  Pack<T, 1> x[ROWS], dt[ROWS], z[ROWS];
+  constexpr int P = VEC ? 1 : 4, W = VEC ? 4 : 1;
+  Pack<float, W> hp[ROWS][P], ap[P];
+  Pack<T, W> bp[ROWS][P], cp[ROWS][P];
   const bool gate = a.z.p != nullptr;
+  const int64_t mine = b0 + (q & (ROWS - 1)), bm = mine < B ? mine : B - 1;
+  const Pack<T, 1> x = load_pack<T, 1>(a.x.row(bm, 0) + c), dt = load_pack<T, 1>(a.dt.row(bm, 0) + c),
+                   z = load_pack<T, 1>((gate ? a.z : a.x).row(bm, 0) + c);
 #pragma unroll
   for (int m = 0; m < ROWS; ++m) {
     const int64_t b = b0 + m < B ? b0 + m : B - 1;
 #pragma unroll
-    for (int k = 0; k < (VEC ? 1 : 4); ++k) {
+    for (int k = 0; k < P; ++k) {
       const int e = k < some ? k : 0;
-      hp[m][k] = load_pack<float, VEC ? 4 : 1>(state + (b * a.C + c) * a.N + n1 + e);
-      bp[m][k] = load_pack<T, VEC ? 4 : 1>(a.bm.row(b, 0) + gn1 + e);
-      cp[m][k] = load_pack<T, VEC ? 4 : 1>(a.cm.row(b, 0) + gn1 + e);
+      hp[m][k] = load_pack<float, W>(state + (b * a.C + c) * a.N + n1 + e);
+      bp[m][k] = load_pack<T, W>(a.bm.row(b, 0) + gn + e);
+      cp[m][k] = load_pack<T, W>(a.cm.row(b, 0) + gn + e);
     }
-    x[m] = load_pack<T, 1>(a.x.row(b, 0) + c);
-    dt[m] = load_pack<T, 1>(a.dt.row(b, 0) + c);
-    z[m] = load_pack<T, 1>((gate ? a.z : a.x).row(b, 0) + c);
   }
 #pragma unroll
-  for (int k = 0; k < (VEC ? 1 : 4); ++k)
-    ap[k] = load_pack<float, VEC ? 4 : 1>(a.A + (int64_t)c * a.N + n1 + (k < some ? k : 0));
+  for (int k = 0; k < P; ++k) ap[k] = load_pack<float, W>(a.A + (int64_t)c * a.N + n1 + (k < some ? k : 0));
   const float D = a.D ? a.D[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+  float s = dt.get(0) + bias;
+  if (a.softplus) s = softplus(s);
+  const float sx = s * x.get(0);
+  float part[ROWS];
 #pragma unroll
   for (int m = 0; m < ROWS; ++m) {
-    float step = dt[m].get(0) + bias;
-    if (a.softplus) step = softplus(step);
-    const float xv = x[m].get(0), sx = step * xv;
-    float h[4], y = 0.f;
+    const float sm = ROWS > 1 ? __shfl_sync(0xffffffffu, s, first + m) : s;
+    const float sxm = ROWS > 1 ? __shfl_sync(0xffffffffu, sx, first + m) : sx;
+    float h[4];
+    part[m] = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int i = VEC ? 0 : k, e = VEC ? k : 0;
-      h[k] = fmaf(ex2(step * (ap[i].get(e) * LOG2E)), hp[m][i].get(e), sx * bp[m][i].get(e));
-      if (k < some) y = fmaf(cp[m][i].get(e), h[k], y);
+      const int v = VEC ? 0 : k, e = VEC ? k : 0;
+      h[k] = fmaf(ex2(sm * (ap[v].get(e) * LOG2E)), hp[m][v].get(e), sxm * bp[m][v].get(e));
+      if (k < some) part[m] = fmaf(cp[m][v].get(e), h[k], part[m]);
     }
-    for (int off = 1; off < lpc; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
     if (on && b0 + m < B) {
       float* st = state + ((b0 + m) * a.C + c) * a.N + n0;
       if (VEC) {
@@ -68,25 +71,37 @@ __global__ void __launch_bounds__(STEP_THREADS) k_selective_step(const Args<T> a
         for (int k = 0; k < 4; ++k)
           if (k < some) st[k] = h[k];
       }
-      if (q == 0) {
-        y = fmaf(D, xv, y);
-        if (gate) y *= silu(z[m].get(0));
-        a.y.row(b0 + m, 0)[c] = from_f32<T>(y);
-      }
     }
+  }
+#pragma unroll
+  for (int half = ROWS / 2; half > 0; half /= 2) {
+    const bool up = (q & half) != 0;
+#pragma unroll
+    for (int m = 0; m < half; ++m) {
+      const float give = up ? part[m] : part[m + half], keep = up ? part[m + half] : part[m];
+      part[m] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+    }
+  }
+  float y = part[0];
+  for (int off = ROWS; off < lpc; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+  if (on && q < ROWS && mine < B) {
+    y = fmaf(D, x.get(0), y);
+    if (gate) y *= silu(z.get(0));
+    a.y.row(mine, 0)[c] = from_f32<T>(y);
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_token_as(Args<T> a, float* state, int64_t B, int lpc, cudaStream_t st) {
-  // Four sequences a lane where that still makes eight blocks for every SM: 256 sequences x 5120 channels bf16 39 us
-  // (0.70 of HBM), with two 43, one 53, eight 44.
-  if (ceil_div(B, 4) * a.C * lpc >= int64_t(148) * 8 * STEP_THREADS) {
+  // four sequences together where a channel has the lanes for it and that still makes eight blocks for every SM
+  if (lpc >= 4 && ceil_div(B, 4) * a.C * lpc >= int64_t(148) * 8 * STEP_THREADS) {
     a.total = (uint32_t)(ceil_div(B, 4) * a.C);
-    k_selective_step<T, VEC, 4><<<(unsigned)ceil_div((int64_t)a.total * lpc, STEP_THREADS), STEP_THREADS, 0, st>>>(a, state, B, lpc);
+    const unsigned blocks = (unsigned)ceil_div((int64_t)a.total * lpc, STEP_THREADS);
+    k_selective_step<T, VEC, 4><<<blocks, STEP_THREADS, 0, st>>>(a, state, B, lpc);
   } else {
     a.total = (uint32_t)(B * a.C);
-    k_selective_step<T, VEC, 1><<<(unsigned)ceil_div((int64_t)a.total * lpc, STEP_THREADS), STEP_THREADS, 0, st>>>(a, state, B, lpc);
+    const unsigned blocks = (unsigned)ceil_div((int64_t)a.total * lpc, STEP_THREADS);
+    k_selective_step<T, VEC, 1><<<blocks, STEP_THREADS, 0, st>>>(a, state, B, lpc);
   }
   return cudaGetLastError();
 }
