@@ -27,7 +27,7 @@ struct Args {
   const int32_t* lengths;
   int64_t B, L, C;
   uint32_t nvec, ntiles, total;
-  int tile;  // tokens per thread, at least W - 1
+  int64_t tile;  // tokens per thread, at least W - 1
 };
 
 template <int W, int VEC, bool SILU>
@@ -200,7 +200,7 @@ cudaError_t launch(const Args<T>& a0, bool use_silu, cudaStream_t st) {
   const int64_t nvec = a.C / VEC;
   int64_t tile = tile_tokens(a.B, a.L, nvec);
   while (a.B * nvec * ceil_div(a.L, tile) > 0x7fff0000) tile *= 2;  // thread indices stay below 2^31
-  a.tile = (int)tile;
+  a.tile = tile;
   a.nvec = (uint32_t)nvec;
   a.ntiles = (uint32_t)ceil_div(a.L, tile);
   a.total = (uint32_t)(a.B * nvec * a.ntiles);
@@ -270,7 +270,7 @@ ssd_status validate(const ssd_conv_dims* d, int64_t seqlen) {
   if (d->width < 2 || d->width > 4) return SSD_ERR_UNSUPPORTED;
   // thread indices stay below 2^31 (a run of tokens per thread can grow, a row cannot)
   if (d->channels > (int64_t(1) << 24) || d->batch > (int64_t(1) << 24) || d->batch * d->channels > 0x7fff0000 ||
-      seqlen > (int64_t(1) << 31))
+      seqlen > 0x7fffffff)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }

@@ -127,7 +127,7 @@ ssd_status validate(const ssd_selective_dims* d, int64_t seqlen) {
     return SSD_ERR_SHAPE;
   // one index per (sequence, channel, lane) stays below 2^31
   if (d->dstate > 128 || d->channels > (int64_t(1) << 24) || d->batch > (int64_t(1) << 24) ||
-      d->batch * d->channels > (int64_t(1) << 25) || seqlen > 0x7fffffff)
+      d->batch * d->channels > (int64_t(1) << 26) || seqlen > 0x7fffffff)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }

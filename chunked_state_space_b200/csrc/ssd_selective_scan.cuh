@@ -47,12 +47,13 @@ struct Args {
   bool softplus, vec, bvec;
 };
 
-// max(v, 0) + log1p(e^-|v|).  The exponent's rounding is put back to first
+// max(v, 0) + log1p(e^-|v|); |v| beyond 128, infinite or the type's lowest, counts
+// as 128, whose e^-|v| is 0.  The exponent's rounding is put back to first
 // order, so that small steps keep f32 accuracy; log1p(e) = e P(e) with P the
 // minimax polynomial of degree 8 of log1p(e) / e on [0, 1] (Remez exchange,
 // P(0) = 1; at most 1.8e-7 off, relative, evaluated in f32).
 __device__ __forceinline__ F2 softplus2(F2 v) {
-  const F2 m{-fabsf(v.x), -fabsf(v.y)}, t = mul2(m, both(LOG2E));
+  const F2 m{fmaxf(-fabsf(v.x), -128.f), fmaxf(-fabsf(v.y), -128.f)}, t = mul2(m, both(LOG2E));
   const F2 p{ex2(t.x), ex2(t.y)};
   const F2 lost = mul2(fma2(m, both(LOG2E), F2{-t.x, -t.y}), both(0.69314718f));
   const F2 e = fma2(p, lost, p);

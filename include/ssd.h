@@ -425,7 +425,11 @@ ssd_status ssd_scan_fwd_vdecay(const ssd_dims* d, const void* x, const float* dt
 /* SSD_CONV_SILU: y = silu(.) instead of the convolution's sum itself. */
 typedef enum { SSD_CONV_SILU = 1 } ssd_conv_flags;
 
-/* batch, seqlen, channels >= 1; width (taps) 2, 3 or 4 (else SSD_ERR_UNSUPPORTED). */
+/*
+ * batch, seqlen, channels >= 1.  Width (taps) 2, 3 or 4, channels and batch at
+ * most 2^24, batch * channels at most 2^31 - 2^16, seqlen < 2^31 (else
+ * SSD_ERR_UNSUPPORTED).
+ */
 typedef struct ssd_conv_dims {
   int64_t batch;    /* B */
   int64_t seqlen;   /* L (not looked at by ssd_conv_step) */
@@ -458,7 +462,11 @@ ssd_status ssd_conv_step(const ssd_conv_dims* d, const void* x, int64_t x_bstrid
 /* SSD_SELECTIVE_SOFTPLUS: the step is softplus(dt + dt_bias) instead of dt + dt_bias. */
 typedef enum { SSD_SELECTIVE_SOFTPLUS = 1 } ssd_selective_flags;
 
-/* batch, seqlen, channels >= 1; 1 <= dstate <= 128 (else SSD_ERR_UNSUPPORTED); ngroups >= 1 dividing channels. */
+/*
+ * batch, seqlen, channels, dstate >= 1; ngroups >= 1 dividing channels.  dstate at
+ * most 128, channels and batch at most 2^24, batch * channels at most 2^26,
+ * seqlen < 2^31 (else SSD_ERR_UNSUPPORTED).
+ */
 typedef struct ssd_selective_dims {
   int64_t batch;    /* B */
   int64_t seqlen;   /* L (not looked at by ssd_selective_step) */
@@ -478,6 +486,8 @@ typedef struct ssd_selective_dims {
  *     s = softplus(dt[b,t,c] + dt_bias[c])          (or dt + dt_bias)
  *     h_t[n] = exp(s A[c,n]) h_{t-1}[n] + s Bm[b,t,g,n] x[b,t,c]
  *     y = sum_n Cm[b,t,g,n] h_t[n] + D[c] x[b,t,c],  times silu(z[b,t,c]) where z is given
+ * A softplus step of -infinity or the type's lowest is 0 and leaves the state as
+ * it is.
  *   x, dt, z, y: rows of C channels (z may be NULL); A [C,N] f32, D, dt_bias
  *   [C] f32 or NULL (= 0);
  *   Bm, Cm: rows of G*N entries with one pair of strides for both;
@@ -499,7 +509,10 @@ ssd_status ssd_selective_step(const ssd_selective_dims* d, const void* x, int64_
                               const float* D, const void* z, int64_t z_bstride, const float* dt_bias, float* state,
                               void* y, int64_t y_bstride, void* stream);
 
-/* batch, seqlen, features >= 1; ngroups >= 1 dividing features, at most 65535; B*L < 2^31 (else SSD_ERR_UNSUPPORTED). */
+/*
+ * batch, seqlen, features >= 1; ngroups >= 1 dividing features.  ngroups at most
+ * 65535, batch * seqlen < 2^31, each size < 2^31 (else SSD_ERR_UNSUPPORTED).
+ */
 typedef struct ssd_norm_dims {
   int64_t batch;    /* B */
   int64_t seqlen;   /* L */

@@ -225,6 +225,31 @@ def test_selective_steps_of_every_size(value):
     close(fin, state, sbound, "f32")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,C,pad", [(2, 48, (0, 0)), (2, 47, (1, 0)), (5, 1024, (0, 0)), (8, 2048, (0, 0))])
+def test_selective_passes_over_masked_steps(io, B, C, pad):
+    """A step of -inf or of the type's lowest value is 0: the tokens around it see the state as if it were not there
+    (bitwise), in the scan and token by token."""
+    d = scan_inputs(io, B, 40, C, 16, 1, seed=57, pad=pad)
+    masked = [0, 7, 8, 20, 39]
+    d["dt"][:, masked] = torch.tensor([float("-inf"), torch.finfo(IO[io]).min, -3e30, -200.0, float("-inf")],
+                                      device="cuda").to(IO[io])[None, :, None]
+    kept = [t for t in range(40) if t not in masked]
+    part = {k: v[:, kept] if k in ("x", "dt", "z", "Bm", "Cm") else v for k, v in d.items()}
+    bc = torch.cat([part["Bm"], part["Cm"]], 2)  # B and C of the kept tokens with one pair of strides
+    part["Bm"], part["Cm"] = bc[:, :, :1], bc[:, :, 1:]
+    st = rnd(58, B, C, 16)
+    y, fin = ssd.ssd_selective_fwd(**d, init_state=st)
+    want, same = ssd.ssd_selective_fwd(**part, init_state=st)
+    assert torch.isfinite(y).all()
+    assert torch.equal(y[:, kept], want) and torch.equal(fin, same)
+    cache = st.clone()
+    for t in (0, 7, 8):
+        ssd.ssd_selective_step(d["x"][:, t], d["dt"][:, t], d["A"], d["Bm"][:, t], d["Cm"][:, t], cache, d["D"],
+                               dt_bias=d["dt_bias"])
+    assert torch.equal(cache, st)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_selective_keeps_what_is_not_finite_to_its_channel(bad):
     d = scan_inputs("f32", 1, 70, 48, 16, 1, seed=55)

@@ -66,7 +66,7 @@ def scan(lib, **o):
 @pytest.mark.parametrize("o,status", [
     (dict(batch=0), 2), (dict(seqlen=0), 2), (dict(channels=0), 2), (dict(dstate=0), 2), (dict(ngroups=0), 2),
     (dict(ngroups=3), 2), (dict(dstate=129), 5), (dict(io=5), 3), (dict(flags=4), 1), (dict(channels=1 << 25), 5),
-    (dict(batch=1 << 13, channels=1 << 13), 5),
+    (dict(batch=1 << 14, channels=1 << 13), 5), (dict(seqlen=1 << 31), 5),
     (dict(x=None), 1), (dict(dt=None), 1), (dict(A=None), 1), (dict(B=None), 1), (dict(C=None), 1), (dict(y=None), 1),
     (dict(dt=at(1, 1)), 4), (dict(A=at(2, 2)), 4), (dict(final=at(11, 2)), 4), (dict(xt=-1), 2), (dict(bct=-16), 2),
     (dict(yt=60), 2), (dict(y=at(0)), 1), (dict(y=at(6, 64)), 1), (dict(y=at(3)), 1), (dict(final=at(8, 64)), 1),
