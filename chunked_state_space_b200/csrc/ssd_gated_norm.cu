@@ -2,14 +2,14 @@
 //   u = x silu(z);  out = weight u / sqrt(mean over the feature's group of u^2 + eps)
 // Bound by HBM: x and z are read once and out is written once.  A run of
 // features (one group of one row) is held in registers as u between the sum
-// and the scaling, PER 16-byte pieces per thread; blocks stay for many rows,
+// and the scaling, up to five 16-byte pieces per thread; blocks stay for many rows,
 // with the next row's loads under way while this one's sum is reduced.  The sum of squares is f32, in a fixed order.
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace gnorm {
 
-constexpr int PER = 5;     // pieces of a row per thread
+constexpr int FIVE = 5;    // pieces of a row per thread of a block
 constexpr int MOST = 640;  // threads of a block (which leaves a thread 96 registers)
 
 template <typename T>
@@ -63,7 +63,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Runs of group blockIdx.y, one at a time per warp (BLOCK false) or block.
-template <typename T, int VEC, bool BLOCK>
+template <typename T, int VEC, bool BLOCK, int PER>
 __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T> a) {
   __shared__ float part[2][MOST / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,17 +160,29 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
   }
 }
 
-// A run of up to 32 * PER pieces takes a warp, a longer one a block of as many
-// warps as hold it; the grid is what the SMs hold at 96 registers a thread.
+// A run of up to 160 pieces takes a warp with as few pieces per thread as hold
+// it (registers for more would cost it warps: 9280 rows of eight runs of 560
+// features bf16 66 us, 85 with five pieces for all), a longer one a block of as
+// many warps as hold it; the grid is what the SMs hold.
 template <typename T, int VEC>
 cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
   const int64_t pieces = a.n / VEC;
   auto blocks = [](int64_t want, int64_t most) { return (unsigned)(want < most ? want : most); };
-  if (pieces <= 32 * PER) {
-    k_gated_norm<T, VEC, false><<<dim3(blocks(ceil_div(a.rows, 4), 148 * 4), groups), 128, 0, st>>>(a);
-  } else if (pieces <= MOST * PER) {
-    const int64_t threads = ceil_div(ceil_div(pieces, PER), 32) * 32;
-    k_gated_norm<T, VEC, true><<<dim3(blocks(a.rows, 148 * (MOST / threads)), groups), (unsigned)threads, 0, st>>>(a);
+  auto warp = [&](auto per, int64_t resident) {
+    k_gated_norm<T, VEC, false, per.value><<<dim3(blocks(ceil_div(a.rows, 4), 148 * resident), groups), 128, 0, st>>>(a);
+  };
+  if (pieces <= 32) {
+    warp(std::integral_constant<int, 1>(), 8);
+  } else if (pieces <= 64) {
+    warp(std::integral_constant<int, 2>(), 6);
+  } else if (pieces <= 96) {
+    warp(std::integral_constant<int, 3>(), 5);
+  } else if (pieces <= 160) {
+    warp(std::integral_constant<int, 5>(), 4);
+  } else if (pieces <= MOST * FIVE) {
+    const int64_t threads = ceil_div(ceil_div(pieces, FIVE), 32) * 32;
+    k_gated_norm<T, VEC, true, FIVE>
+        <<<dim3(blocks(a.rows, 148 * (MOST / threads)), groups), (unsigned)threads, 0, st>>>(a);
   } else {
     k_gated_norm_long<T, VEC><<<dim3((unsigned)a.rows, groups), MOST, 0, st>>>(a);
   }

@@ -623,12 +623,10 @@ cudaError_t launch_teams(Args<T> a, int64_t B, cudaStream_t st) {
       return cudaGetLastError();
     }
   }
-  if constexpr (NS > 1) {
-    if (a.vec)
-      k_selective_teams<T, NS, LPC, true, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
-    else
-      k_selective_teams<T, NS, LPC, false, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
-  }
+  if (a.vec)
+    k_selective_teams<T, NS, LPC, true, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
+  else
+    k_selective_teams<T, NS, LPC, false, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -658,12 +656,12 @@ cudaError_t launch_prompt(Args<T> a, int64_t B, cudaStream_t st) {
   // them with tokens, 1530 channels: 42 us with teams, 52 with many).
   const int64_t channels = a.lengths ? ceil_div(B * a.C, 2) : B * a.C;
   auto warps = [&](int lpc) { return channels * lpc / 32; };
-  // 10240 channels, 1024 tokens, 8 states 81 us with many as with teams; 768 channels 58 and 41
+  // 16 lanes, one entry to each: 768 channels of 2048 tokens 44 us, with 8 lanes 67 (4096 channels of 1024: 65 and
+  // 50); also for fewer entries than lanes (4 states, 770 channels of 14400 tokens: 461 us, with 4 lanes 1129)
+  if (a.N <= 16 && warps(16) <= 2 * SCHEDULERS) return launch_teams<T, 1, 16>(a, B, st);
+  // 8 states, 10240 channels of 1024 tokens: 81 us, with many as much (768 channels 41 and 58)
   if (a.N <= 8) return launch_teams<T, 2, 4>(a, B, st);
   if (a.N <= 16) {
-    // 16 lanes: 768 channels of 2048 tokens 44 us, with 8 lanes 67 (4096 channels of 1024: 65 and 50); only for whole
-    // pieces, as the helpers cannot keep up element by element
-    if (a.vec && a.bvec && warps(16) <= 2 * SCHEDULERS) return launch_teams<T, 1, 16>(a, B, st);
     // 4096 channels of 1024 tokens 50 us, with many 53 (7680 channels: 96 and 83)
     if (warps(8) <= 2 * SCHEDULERS) return launch_teams<T, 2, 8>(a, B, st);
     // 10240 channels of 2048 tokens 195 us, with 4 lanes 215 (40960 channels: 667 and 559)
