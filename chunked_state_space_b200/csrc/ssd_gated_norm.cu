@@ -62,6 +62,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// A run of at most 16 pieces: a piece to a thread, `lanes` threads (a power of
+// two) to a run, neighbouring groups side by side.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_gated_norm_short(const Args<T> a, uint32_t groups, uint32_t runs, int lanes) {
+  const uint32_t run = blockIdx.x * (256u / lanes) + threadIdx.x / lanes;
+  const int p = threadIdx.x & (lanes - 1);
+  const bool on = run < runs && p * VEC < a.n;  // the others take part in the shuffles
+  const uint32_t row = run / groups, g = run - row * groups, b = row / a.L, t = row - b * a.L;
+  const int64_t f = (int64_t)g * a.n + p * VEC;  // the piece's first feature
+  float u[VEC] = {}, w[VEC], ss = 0.f;
+  if (on) {
+    const bool gate = a.z.p != nullptr;
+    const Pack<T, VEC> x = load_pack<T, VEC>(a.x.row(b, t) + f), z = load_pack<T, VEC>((gate ? a.z : a.x).row(b, t) + f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = 1.f;
+    if (a.weight) load_params<VEC, (VEC > 1)>(a.weight + f, w);
+    ss = gated(x, z, gate, u);
+  }
+  for (int off = lanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if (on) {
+    scaled(u, 1.0f / sqrtf(ss / (float)a.n + a.eps), w);
+    store_pack<T, VEC>(a.out.row(b, t) + f, to_pack<T, VEC>(u));
+  }
+}
+
 // Runs of group blockIdx.y, one at a time per warp (BLOCK false) or block.
 template <typename T, int VEC, bool BLOCK, int PER>
 __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T> a) {
@@ -160,7 +185,8 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
   }
 }
 
-// A run of up to 160 pieces takes a warp with as few pieces per thread as hold
+// A run of up to 16 pieces takes part of a warp (16384 rows of eight runs of
+// eight features bf16 4 us, 34 with a warp each), one of up to 160 a warp with as few pieces per thread as hold
 // it (registers for more would cost it warps: 9280 rows of eight runs of 560
 // features bf16 66 us, 85 with five pieces for all), a longer one a block of as
 // many warps as hold it; the grid is what the SMs hold.
@@ -171,7 +197,12 @@ cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
   auto warp = [&](auto per, int64_t resident) {
     k_gated_norm<T, VEC, false, per.value><<<dim3(blocks(ceil_div(a.rows, 4), 148 * resident), groups), 128, 0, st>>>(a);
   };
-  if (pieces <= 32) {
+  if (pieces <= 16 && a.rows * groups <= 0x7fffffff) {
+    int lanes = 1;
+    while (lanes < pieces) lanes *= 2;
+    const int64_t runs = a.rows * groups;
+    k_gated_norm_short<T, VEC><<<(unsigned)ceil_div(runs, 256 / lanes), 256, 0, st>>>(a, groups, (uint32_t)runs, lanes);
+  } else if (pieces <= 32) {
     warp(std::integral_constant<int, 1>(), 8);
   } else if (pieces <= 64) {
     warp(std::integral_constant<int, 2>(), 6);

@@ -326,6 +326,10 @@ def test_selective_offsets_past_32_bits():
     (3, 4, 1530, 2, (0, 0), True, True), (2, 9, 1024, 1, (0, 8), False, True), (1, 6, 1040, 1, (8, 0), True, True),
     (2, 3, 5120, 1, (0, 0), True, True), (1, 2, 5121, 1, (0, 0), True, True), (1, 2, 32768 + 8, 1, (0, 0), True, True),
     (2, 2, 9000, 2, (1, 0), True, True), (1, 2, 48, 48, (0, 0), False, False),
+    # parts of a warp, and each number of pieces that a warp holds
+    (3, 67, 64, 8, (0, 0), True, True), (2, 33, 192, 3, (8, 0), False, True), (2, 5, 130, 10, (1, 0), True, True),
+    (5, 41, 256, 1, (0, 0), True, True), (2, 700, 512, 1, (0, 0), True, True), (2, 9, 760, 1, (0, 0), True, False),
+    (700, 3, 1160, 1, (0, 0), True, True), (3, 3, 1288, 1, (0, 0), True, True), (1500, 2, 2568, 1, (8, 8), True, True),
 ])
 def test_gated_norm_matches_64_bits(io, B, L, F, G, pad, gate, weighted):
     x, z = rnd(100, B, L, F, io=io), rnd(101, B, L, F, io=io) if gate else None
