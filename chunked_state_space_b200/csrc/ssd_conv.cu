@@ -5,8 +5,8 @@
 //
 // Bound by HBM: each element is read once and written once, against about a
 // dozen fp32 operations and two special-function ones (e^-v and a reciprocal).
-// A thread owns 16 bytes of channels (one element where rows are not 16-byte
-// aligned) and a run of consecutive tokens, and keeps the last W-1 inputs in
+// A thread owns 16 bytes of channels (two elements or one where rows are not
+// 16-byte aligned) and a run of consecutive tokens, and keeps the last W-1 inputs in
 // registers, so a tap costs no further load; only the W-1 rows before a run
 // are read twice.
 #include "ssd_rows.cuh"
@@ -35,14 +35,14 @@ struct Taps {
   float w[W][VEC], b[VEC];
   __device__ __forceinline__ void load(const float* weight, const float* bias, int64_t c) {
     float rows[VEC * W];
-    load_params<VEC * W, (VEC > 1)>(weight + c * W, rows);
+    load_params<VEC * W, (VEC >= 4)>(weight + c * W, rows);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
 #pragma unroll
       for (int k = 0; k < W; ++k) w[k][i] = rows[i * W + k];
       b[i] = 0.f;
     }
-    if (bias) load_params<VEC, (VEC > 1)>(bias + c, b);
+    if (bias) load_params<VEC, (VEC >= 4)>(bias + c, b);
   }
   // old[0] is the oldest of the W-1 inputs before `in`
   template <typename T>
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, AHEAD == 8 ? 3 : 4) k_conv_fwd(const 
   for (; t < t1; ++t, x += a.x.ts) token(load_pack<T, VEC>(x));
 }
 
-// One token: a thread takes 16 bytes of channels (or one) of up to ROWS
+// One token: a thread takes as many channels of up to ROWS
 // sequences, with their weights loaded once.
 template <typename T, int W, int VEC, bool SILU, int ROWS>
 __global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, int64_t xbs, const float* weight,
@@ -245,9 +245,10 @@ cudaError_t launch_step(const ssd_conv_dims* d, const void* x, int64_t xbs, cons
   return cudaGetLastError();
 }
 
-// f(T, W, VEC) for the call's type, width and alignment.
+// f(T, W, VEC) for the call's type, width and alignment: 16-byte pieces (vec
+// 2), pairs of elements (1) or single ones (0).
 template <typename F>
-cudaError_t dispatch(int io, int64_t width, bool vec, F&& f) {
+cudaError_t dispatch(int io, int64_t width, int vec, F&& f) {
   auto with_width = [&](auto t, auto v) {
     switch (width) {
       case 2: return f(t, std::integral_constant<int, 2>(), v);
@@ -255,11 +256,13 @@ cudaError_t dispatch(int io, int64_t width, bool vec, F&& f) {
       default: return f(t, std::integral_constant<int, 4>(), v);
     }
   };
-  if (io == SSD_BF16)
-    return vec ? with_width(__nv_bfloat16(), std::integral_constant<int, 8>())
-               : with_width(__nv_bfloat16(), std::integral_constant<int, 1>());
-  return vec ? with_width(float(), std::integral_constant<int, 4>())
-             : with_width(float(), std::integral_constant<int, 1>());
+  auto with_type = [&](auto t, auto whole) {
+    if (vec == 2) return with_width(t, whole);
+    if (vec == 1) return with_width(t, std::integral_constant<int, 2>());
+    return with_width(t, std::integral_constant<int, 1>());
+  };
+  return io == SSD_BF16 ? with_type(__nv_bfloat16(), std::integral_constant<int, 8>())
+                        : with_type(float(), std::integral_constant<int, 4>());
 }
 
 ssd_status validate(const ssd_conv_dims* d, int64_t seqlen) {
@@ -301,8 +304,11 @@ extern "C" ssd_status ssd_conv_fwd(const ssd_conv_dims* d, const void* x, int64_
     if (spans_meet(sy, in) || spans_meet(sf, in)) return SSD_ERR_INVALID_ARG;
   if (spans_meet(sy, si) || spans_meet(sy, sf) || (final_state != init_state && spans_meet(sf, si)))
     return SSD_ERR_INVALID_ARG;
-  const bool vec = rows_on_16(rx, B, L, es) && rows_on_16(ry, B, L, es) && rows_on_16(ri, B, W - 1, es) &&
-                   rows_on_16(rf, B, W - 1, es) && on_16(weight) && on_16(bias);
+  auto on = [&](size_t bytes) {
+    return rows_on(rx, B, L, es, bytes) && rows_on(ry, B, L, es, bytes) && rows_on(ri, B, W - 1, es, bytes) &&
+           rows_on(rf, B, W - 1, es, bytes);
+  };
+  const int vec = on(16) && on_16(weight) && on_16(bias) ? 2 : on(2 * es) ? 1 : 0;
   return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
     using T = decltype(t);
     conv::Args<T> a{};
@@ -336,8 +342,10 @@ extern "C" ssd_status ssd_conv_step(const ssd_conv_dims* d, const void* x, int64
   for (const Span& in : {sx, sw, sb})
     if (spans_meet(sy, in) || spans_meet(ss, in)) return SSD_ERR_INVALID_ARG;
   if (spans_meet(sy, ss)) return SSD_ERR_INVALID_ARG;
-  const bool vec = rows_on_16(rx, B, 1, es) && rows_on_16(ry, B, 1, es) && rows_on_16(rs, B, W - 1, es) &&
-                   on_16(weight) && on_16(bias);
+  auto on = [&](size_t bytes) {
+    return rows_on(rx, B, 1, es, bytes) && rows_on(ry, B, 1, es, bytes) && rows_on(rs, B, W - 1, es, bytes);
+  };
+  const int vec = on(16) && on_16(weight) && on_16(bias) ? 2 : on(2 * es) ? 1 : 0;
   return cuda_status(conv::dispatch(d->io_dtype, W, vec, [&](auto t, auto w, auto v) {
     return conv::launch_step<decltype(t), w.value, v.value>(d, x, x_bstride, weight, bias, state, y, y_bstride,
                                                             static_cast<cudaStream_t>(stream));

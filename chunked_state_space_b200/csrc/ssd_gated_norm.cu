@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) k_gated_norm_short(const Args<T> a, uint3
     const Pack<T, VEC> x = load_pack<T, VEC>(a.x.row(b, t) + f), z = load_pack<T, VEC>((gate ? a.z : a.x).row(b, t) + f);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = 1.f;
-    if (a.weight) load_params<VEC, (VEC > 1)>(a.weight + f, w);
+    if (a.weight) load_params<VEC, (VEC >= 4)>(a.weight + f, w);
     ss = gated(x, z, gate, u);
   }
   for (int off = lanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(BLOCK ? MOST : 128) k_gated_norm(const Args<T>
   auto weights = [&](int k, float (&w)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = 1.f;
-    if (a.weight && me + k * all < pieces) load_params<VEC, (VEC > 1)>(a.weight + g0 + (int64_t)(me + k * all) * VEC, w);
+    if (a.weight && me + k * all < pieces) load_params<VEC, (VEC >= 4)>(a.weight + g0 + (int64_t)(me + k * all) * VEC, w);
   };
   float held[BLOCK ? 1 : PER][VEC];
   if constexpr (!BLOCK) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
     float w[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = 1.f;
-    if (a.weight) load_params<VEC, (VEC > 1)>(a.weight + g0 + p * VEC, w);
+    if (a.weight) load_params<VEC, (VEC >= 4)>(a.weight + g0 + p * VEC, w);
     scaled(u, inv, w);
     store_pack<T, VEC>(out + p * VEC, to_pack<T, VEC>(u));
   }
@@ -243,8 +243,10 @@ extern "C" ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, i
       sz{z, z ? row_extent(rz, B, L, es) : 0}, sw{weight, sizeof(float) * F};
   const bool in_place = x == out && (B == 1 || x_bstride == out_bstride) && (L == 1 || x_tstride == out_tstride);
   if ((!in_place && spans_meet(so, sx)) || spans_meet(so, sz) || spans_meet(so, sw)) return SSD_ERR_INVALID_ARG;
-  bool vec = rows_on_16(rx, B, L, es) && rows_on_16(ro, B, L, es) && (!z || rows_on_16(rz, B, L, es));
-  vec = vec && (F / G * es) % 16 == 0 && on_16(weight);
+  auto on = [&](size_t bytes) {
+    return rows_on(rx, B, L, es, bytes) && rows_on(ro, B, L, es, bytes) && (!z || rows_on(rz, B, L, es, bytes)) &&
+           (F / G * es) % bytes == 0;
+  };
   auto go = [&](auto t, auto v) {
     using T = decltype(t);
     gnorm::Args<T> a{};
@@ -258,9 +260,11 @@ extern "C" ssd_status ssd_rmsnorm_gated(const ssd_norm_dims* d, const void* x, i
     a.n = F / G;
     return gnorm::launch<T, v.value>(a, (unsigned)G, static_cast<cudaStream_t>(stream));
   };
-  if (d->io_dtype == SSD_BF16)
-    return cuda_status(vec ? go(__nv_bfloat16(), std::integral_constant<int, 8>())
-                           : go(__nv_bfloat16(), std::integral_constant<int, 1>()));
-  return cuda_status(vec ? go(float(), std::integral_constant<int, 4>())
-                         : go(float(), std::integral_constant<int, 1>()));
+  auto pieces = [&](auto t, auto whole) {
+    if (on(16) && on_16(weight)) return go(t, whole);
+    if (on(2 * es)) return go(t, std::integral_constant<int, 2>());
+    return go(t, std::integral_constant<int, 1>());
+  };
+  return cuda_status(d->io_dtype == SSD_BF16 ? pieces(__nv_bfloat16(), std::integral_constant<int, 8>())
+                                             : pieces(float(), std::integral_constant<int, 4>()));
 }

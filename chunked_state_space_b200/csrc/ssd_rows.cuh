@@ -15,8 +15,8 @@ struct Rows {
   __device__ __forceinline__ T* row(int64_t b, int64_t t) const { return p + b * bs + t * ts; }
 };
 
-// VEC consecutive elements as one access moves them: 16 bytes (8: four f32's
-// worth of bf16), or one element where rows do not start on 16 bytes.  Kept as
+// VEC consecutive elements as one access moves them: 16 bytes, or two elements
+// or one where rows do not start on 16 bytes (four bf16 beside four f32).  Kept as
 // whole words until an element is asked for: unpacked where they are loaded,
 // each load would be waited for on the spot.
 template <typename T, int VEC>
@@ -38,6 +38,21 @@ struct alignas(8) Pack<__nv_bfloat16, 4> {
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+};
+template <>
+struct alignas(4) Pack<__nv_bfloat16, 2> {
+  uint32_t w;
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16); }
+  __device__ __forceinline__ void set2(int, float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    w = *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <>
+struct alignas(8) Pack<float, 2> {
+  float w[2];
+  __device__ __forceinline__ float get(int i) const { return w[i]; }
+  __device__ __forceinline__ void set2(int, float lo, float hi) { w[0] = lo, w[1] = hi; }
 };
 template <>
 struct alignas(16) Pack<float, 4> {
@@ -183,11 +198,12 @@ inline ssd_status check_rows(const RowArg& r, int64_t B, int64_t L, size_t es, b
   return (reinterpret_cast<uintptr_t>(r.p) & (es - 1)) ? SSD_ERR_ALIGN : SSD_OK;
 }
 
-// Whether every row can be read in 16-byte pieces.
-inline bool rows_on_16(const RowArg& r, int64_t B, int64_t L, size_t es) {
-  return (reinterpret_cast<uintptr_t>(r.p) & 15u) == 0 && (B == 1 || (r.bs * es) % 16 == 0) &&
-         (L == 1 || (r.ts * es) % 16 == 0) && (r.width * es) % 16 == 0;
+// Whether every row can be read in pieces of `bytes`.
+inline bool rows_on(const RowArg& r, int64_t B, int64_t L, size_t es, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(r.p) % bytes == 0 && (B == 1 || (r.bs * es) % bytes == 0) &&
+         (L == 1 || (r.ts * es) % bytes == 0) && (r.width * es) % bytes == 0;
 }
+inline bool rows_on_16(const RowArg& r, int64_t B, int64_t L, size_t es) { return rows_on(r, B, L, es, 16); }
 
 struct Span {
   const void* p;

@@ -53,6 +53,9 @@ def lens(values):
     (2, 3, 5, 3, (0, 0), False, False, [5, 0, 1]),
     (3, 3, 33, 16, (0, 0), True, True, [40, -3, 17]),     # lengths outside [0, L] are taken into it
     (4, 2, 700, 1800, (0, 0), True, True, [700, 333]),    # longer runs of tokens per thread
+    (4, 3, 70, 1802, (2, 4), True, True, [70, 69, 1]),    # pairs of elements
+    (3, 2, 67, 1801, (1, 4), True, True, None),           # single ones
+    (2, 2, 66, 14, (6, 0), False, True, None),
 ])
 def test_conv_matches_64_bits(io, width, B, L, C, pad, silu, init, lengths):
     x, w, b = rnd(1, B, L, C, io=io), rnd(2, C, width), rnd(3, C)
@@ -79,7 +82,7 @@ def test_conv_matches_64_bits(io, width, B, L, C, pad, silu, init, lengths):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("width,C", [(4, 48), (3, 7), (2, 16)])
+@pytest.mark.parametrize("width,C", [(4, 48), (3, 7), (2, 16), (4, 50)])
 def test_conv_in_pieces_and_by_tokens_is_the_whole(io, width, C):
     """A prompt in pieces, its cache updated in place, then token by token: bitwise one call over all tokens."""
     x, w, b = rnd(5, 2, 40, C, io=io), rnd(6, C, width), rnd(7, C)
@@ -330,6 +333,8 @@ def test_selective_offsets_past_32_bits():
     (3, 67, 64, 8, (0, 0), True, True), (2, 33, 192, 3, (8, 0), False, True), (2, 5, 130, 10, (1, 0), True, True),
     (5, 41, 256, 1, (0, 0), True, True), (2, 700, 512, 1, (0, 0), True, True), (2, 9, 760, 1, (0, 0), True, False),
     (700, 3, 1160, 1, (0, 0), True, True), (3, 3, 1288, 1, (0, 0), True, True), (1500, 2, 2568, 1, (8, 8), True, True),
+    # pairs of elements
+    (3, 4, 1530, 1, (2, 2), True, True), (2, 3, 130, 5, (4, 2), True, True), (1, 2, 13002, 1, (2, 0), True, True),
 ])
 def test_gated_norm_matches_64_bits(io, B, L, F, G, pad, gate, weighted):
     x, z = rnd(100, B, L, F, io=io), rnd(101, B, L, F, io=io) if gate else None
