@@ -6,9 +6,9 @@
 // Bound by HBM: each element is read once and written once, against about a
 // dozen fp32 operations and two special-function ones (e^-v and a reciprocal).
 // A thread owns 16 bytes of channels (two elements or one where rows are not
-// 16-byte aligned) and a run of consecutive tokens, and keeps the last W-1 inputs in
-// registers, so a tap costs no further load; only the W-1 rows before a run
-// are read twice.
+// 16-byte aligned) and a run of consecutive tokens, and keeps the last W-1
+// inputs in registers, so a tap costs no further load; only the W-1 rows before
+// a run are read twice.
 #include "ssd_rows.cuh"
 
 namespace ssd {
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(THREADS, AHEAD == 8 ? 3 : 4) k_conv_fwd(const 
   for (; t < t1; ++t, x += a.x.ts) token(load_pack<T, VEC>(x));
 }
 
-// One token: a thread takes as many channels of up to ROWS
-// sequences, with their weights loaded once.
+// One token: a thread takes as many channels of up to ROWS sequences, with
+// their weights loaded once.
 template <typename T, int W, int VEC, bool SILU, int ROWS>
 __global__ void __launch_bounds__(THREADS) k_conv_step(const T* __restrict__ x, int64_t xbs, const float* weight,
                                                        const float* bias, T* state, T* __restrict__ y, int64_t ybs,
@@ -232,8 +232,9 @@ cudaError_t launch_step(const ssd_conv_dims* d, const void* x, int64_t xbs, cons
     k_conv_step<T, W, VEC, silu.value, rows.value><<<(total + THREADS - 1) / THREADS, THREADS, 0, st>>>(
         (const T*)x, xbs, weight, bias, (T*)state, (T*)y, ybs, d->batch, d->channels, (uint32_t)nvec, total);
   };
-  // four sequences a thread where that still makes a block for every SM
-  const bool many = ceil_div(d->batch, 4) * nvec >= 148 * THREADS;
+  // Four sequences a thread where that still makes a block for every other SM: 64 sequences of 5376 channels bf16
+  // 2.8 us, 3.4 with one each, 256 5.1 and 8.2 (64 of 1792 channels: 2.7 and 2.1).
+  const bool many = ceil_div(d->batch, 4) * nvec >= 74 * THREADS;
   auto pick = [&](auto silu) {
     if (many)
       go(silu, std::integral_constant<int, 4>());

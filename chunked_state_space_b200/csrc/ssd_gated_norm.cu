@@ -2,8 +2,9 @@
 //   u = x silu(z);  out = weight u / sqrt(mean over the feature's group of u^2 + eps)
 // Bound by HBM: x and z are read once and out is written once.  A run of
 // features (one group of one row) is held in registers as u between the sum
-// and the scaling, up to five 16-byte pieces per thread; blocks stay for many rows,
-// with the next row's loads under way while this one's sum is reduced.  The sum of squares is f32, in a fixed order.
+// and the scaling, up to five 16-byte pieces per thread; blocks stay for many
+// rows, with the next row's loads under way while this one's sum is reduced.
+// The sum of squares is f32, in a fixed order.
 #include "ssd_rows.cuh"
 
 namespace ssd {
@@ -186,10 +187,11 @@ __global__ void __launch_bounds__(MOST) k_gated_norm_long(const Args<T> a) {
 }
 
 // A run of up to 16 pieces takes part of a warp (16384 rows of eight runs of
-// eight features bf16 4 us, 34 with a warp each), one of up to 160 a warp with as few pieces per thread as hold
-// it (registers for more would cost it warps: 9280 rows of eight runs of 560
-// features bf16 66 us, 85 with five pieces for all), a longer one a block of as
-// many warps as hold it; the grid is what the SMs hold.
+// eight features bf16 4 us, 34 with a warp each), one of up to 160 a warp with
+// as few pieces per thread as hold it (registers for more would cost it warps:
+// 9280 rows of eight runs of 560 features bf16 66 us, 85 with five pieces for
+// all), a longer one a block of as many warps as hold it; the grid is what the
+// SMs hold.
 template <typename T, int VEC>
 cudaError_t launch(const Args<T>& a, unsigned groups, cudaStream_t st) {
   const int64_t pieces = a.n / VEC;

@@ -101,7 +101,8 @@ def gated_norm(x, z, weight, eps, ngroups):
     ms = np.mean(v * v, -1, keepdims=True)
     out = (v / np.sqrt(ms + eps)).reshape(x.shape) * weight
     # sum of squares: each term off by twice its factor's error (weighted by its square) and by the roundings along
-    # its path: the elements of one thread (of 512 at least where the run is long, else at most 40), 5 shuffles, 20 warps; then mean, eps, root and reciprocal
+    # its path: the elements of one thread (of 512 at least where the run is long, else at most 40), 5 shuffles, 20
+    # warps; then mean, eps, root and reciprocal
     path = F // ngroups // 512 + 40 + 5 + 20
     r = rel.reshape(v.shape)
     dm = np.sum(v * v * 2 * r, -1, keepdims=True) / np.maximum(np.sum(v * v, -1, keepdims=True), 1e-300) + path * U
