@@ -139,6 +139,8 @@ struct Call {
   float* final_state;
   const int32_t* lengths;
   float* state;
+  void* workspace;
+  size_t workspace_bytes;
 };
 
 ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream_t st) {
@@ -152,17 +154,22 @@ ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream
   for (const void* p : {(const void*)k.A, (const void*)k.D, (const void*)k.dt_bias, (const void*)k.init,
                         (const void*)k.final_state, (const void*)k.lengths})
     if (!f32_aligned(p)) return SSD_ERR_ALIGN;
+  const size_t scratch = k.workspace ? segment_bytes(d) : 0;
+  if (!on_16(k.workspace)) return SSD_ERR_ALIGN;
+  if (k.workspace && k.workspace_bytes < scratch) return SSD_ERR_WORKSPACE;
   const size_t state = sizeof(float) * B * C * N;
   const Span sy{k.y.p, row_extent(k.y, B, L, es)}, sf{k.final_state, state}, si{k.init, state};
+  const Span sw{scratch ? k.workspace : nullptr, scratch};
   for (const RowArg* r : {&k.x, &k.dt, &k.z, &k.bm, &k.cm}) {
     const Span in{r->p, r->p ? row_extent(*r, B, L, es) : 0};
-    if (spans_meet(sy, in) || spans_meet(sf, in)) return SSD_ERR_INVALID_ARG;
+    if (spans_meet(sy, in) || spans_meet(sf, in) || spans_meet(sw, in)) return SSD_ERR_INVALID_ARG;
   }
   for (const Span& in : {Span{k.A, sizeof(float) * C * N}, Span{k.D, sizeof(float) * C},
                          Span{k.dt_bias, sizeof(float) * C}, Span{k.lengths, sizeof(int32_t) * B}})
-    if (spans_meet(sy, in) || spans_meet(sf, in)) return SSD_ERR_INVALID_ARG;
+    if (spans_meet(sy, in) || spans_meet(sf, in) || spans_meet(sw, in)) return SSD_ERR_INVALID_ARG;
   if (spans_meet(sy, si) || spans_meet(sy, sf) || (k.init != k.final_state && spans_meet(sf, si)))
     return SSD_ERR_INVALID_ARG;
+  if (spans_meet(sw, sy) || spans_meet(sw, sf) || spans_meet(sw, si)) return SSD_ERR_INVALID_ARG;
   auto go = [&](auto t) {
     using T = decltype(t);
     auto rows = [](const RowArg& r) { return Rows<const T>{(const T*)r.p, r.bs, r.ts}; };
@@ -179,7 +186,10 @@ ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream
     a.init = k.init;
     a.final_state = k.final_state;
     a.lengths = k.lengths;
+    a.B = B;
     a.L = L;
+    a.nseg = 1;
+    a.seg_len = L;
     a.C = (int)C;
     a.N = (int)N;
     a.G = (int)d->ngroups;
@@ -190,7 +200,7 @@ ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream
     for (const RowArg* r : {&k.x, &k.dt, &k.z, &k.y})
       if (r->p && !rows_on_16(*r, B, L, es)) a.vec = false;
     a.bvec = rows_on_16(k.bm, B, L, es) && rows_on_16(k.cm, B, L, es);
-    return launch_prompt<T>(a, B, st);
+    return launch_prompt<T>(a, B, d, scratch ? k.workspace : nullptr, st);
   };
   return cuda_status(d->io_dtype == SSD_BF16 ? go(__nv_bfloat16()) : go(float()));
 }
@@ -198,20 +208,29 @@ ssd_status run(const ssd_selective_dims* d, int64_t L, const Call& k, cudaStream
 }  // namespace selective
 }  // namespace ssd
 
+extern "C" ssd_status ssd_selective_workspace_size(const ssd_selective_dims* d, size_t* bytes) {
+  using namespace ssd;
+  if (!bytes) return SSD_ERR_INVALID_ARG;
+  const ssd_status s = selective::validate(d, d ? d->seqlen : 1);
+  if (s != SSD_OK) return s;
+  *bytes = selective::segment_bytes(d);
+  return SSD_OK;
+}
+
 extern "C" ssd_status ssd_selective_fwd(const ssd_selective_dims* d, const void* x, int64_t x_bstride,
                                         int64_t x_tstride, const void* dt, int64_t dt_bstride, int64_t dt_tstride,
                                         const float* A, const void* Bm, const void* Cm, int64_t bc_bstride,
                                         int64_t bc_tstride, const float* D, const void* z, int64_t z_bstride,
                                         int64_t z_tstride, const float* dt_bias, const float* init_state,
                                         const int32_t* lengths, void* y, int64_t y_bstride, int64_t y_tstride,
-                                        float* final_state, void* stream) {
+                                        float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace ssd;
   const ssd_status s = selective::validate(d, d ? d->seqlen : 1);
   if (s != SSD_OK) return s;
   const int64_t C = d->channels, gn = d->ngroups * d->dstate;
   const selective::Call k{{x, x_bstride, x_tstride, C},   {dt, dt_bstride, dt_tstride, C}, {z, z_bstride, z_tstride, C},
                           {Bm, bc_bstride, bc_tstride, gn}, {Cm, bc_bstride, bc_tstride, gn}, {y, y_bstride, y_tstride, C},
-                          A, D, dt_bias, init_state, final_state, lengths, nullptr};
+                          A, D, dt_bias, init_state, final_state, lengths, nullptr, workspace, workspace_bytes};
   return selective::run(d, d->seqlen, k, static_cast<cudaStream_t>(stream));
 }
 
@@ -227,6 +246,6 @@ extern "C" ssd_status ssd_selective_step(const ssd_selective_dims* d, const void
   const int64_t C = d->channels, gn = d->ngroups * d->dstate;
   const selective::Call k{{x, x_bstride, 0, C},   {dt, dt_bstride, 0, C}, {z, z_bstride, 0, C},
                           {Bm, bc_bstride, 0, gn}, {Cm, bc_bstride, 0, gn}, {y, y_bstride, 0, C},
-                          A, D, dt_bias, state, state, nullptr, state};
+                          A, D, dt_bias, state, state, nullptr, state, nullptr, 0};
   return selective::run(d, 1, k, static_cast<cudaStream_t>(stream));
 }

@@ -22,7 +22,11 @@
 //       scheduler has few warps;
 //   k_selective_many   every warp does everything, phase by phase: fewer
 //       registers and no idle warps, which counts where blocks fill the SMs.
+// Long sequences of few channels are cut into segments that run at once
+// (segments, below).
 #pragma once
+
+#include <algorithm>
 
 #include "ssd_rows.cuh"
 
@@ -32,6 +36,7 @@ namespace selective {
 constexpr int LANES = 128;  // lanes of a block that carry the recurrence
 constexpr int HELPERS = 64, TEAM_THREADS = LANES + 2 * HELPERS;
 constexpr int64_t SCHEDULERS = 4 * 148;  // warp schedulers of the GPU
+constexpr int MAX_SEGMENTS = 64;
 
 template <typename T>
 struct Args {
@@ -41,10 +46,15 @@ struct Args {
   const float* init;
   float* final_state;
   const int32_t* lengths;
-  int64_t L;
+  int64_t B, L;
   int C, N, G, per_group;
   uint32_t blocks_per_group, total;
   bool softplus, vec, bvec;
+  // Segments of seg_len tokens of every sequence (1: the whole sequences).  With more than one, starts [nseg,B,C,N]
+  // holds the state that each begins with, sums [nseg - 1,B,C] the steps that it takes in all.
+  int nseg;
+  int64_t seg_len;
+  float *starts, *sums;
 };
 
 // max(v, 0) + log1p(e^-|v|); |v| beyond 128, infinite or the type's lowest, counts
@@ -217,40 +227,50 @@ __device__ __forceinline__ Pack<T, V> outputs(const Pack<T, V>& x, const Pack<T,
   return to_pack<T, V>(out);
 }
 
-// The block's channels and sequence, and a lane's rates and states.
+// The block's segment of a sequence and its channels, and a lane's rates and
+// states.
 template <int CB>
 struct Place {
-  uint32_t b, g;
+  uint32_t b, g, seg;
   int c0, nc;  // first channel, how many
+  int64_t t0;  // first token
   int len;     // tokens
 };
 template <int CB, typename T>
 __device__ __forceinline__ Place<CB> place(const Args<T>& a) {
   Place<CB> p;
-  const uint32_t r = blockIdx.x / a.blocks_per_group, cb = blockIdx.x - r * a.blocks_per_group;
-  p.b = r / a.G;
-  p.g = r - p.b * a.G;
+  uint32_t r = blockIdx.x / a.blocks_per_group;
+  const uint32_t cb = blockIdx.x - r * a.blocks_per_group;
+  p.g = r % (uint32_t)a.G;
+  r /= (uint32_t)a.G;
+  p.b = a.nseg == 1 ? r : r % (uint32_t)a.B;
+  p.seg = a.nseg == 1 ? 0 : r / (uint32_t)a.B;
   p.c0 = (int)p.g * a.per_group + (int)cb * CB;
   p.nc = min(CB, ((int)p.g + 1) * a.per_group - p.c0);
-  p.len = (int)row_length(a.lengths, p.b, a.L);
+  p.t0 = p.seg * a.seg_len;
+  const int64_t rest = row_length(a.lengths, p.b, a.L) - p.t0;
+  p.len = (int)(rest < 0 ? 0 : rest < a.seg_len ? rest : a.seg_len);
   return p;
 }
 template <int NS, int CB, typename T>
-__device__ __forceinline__ void begin(const Args<T>& a, const Place<CB>& p, int ch, int q, float (&A2)[NS], float (&h)[NS]) {
+__device__ __forceinline__ void begin(const Args<T>& a, const Place<CB>& p, int ch, int q, float (&A2)[NS], float (&h)[NS],
+                                      bool from_zero = false) {
+  const float* from = from_zero ? nullptr : a.nseg == 1 ? a.init : a.starts + (int64_t)p.seg * a.B * a.C * a.N;
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const int n = q * NS + k;
     const bool in = ch < p.nc && n < a.N;
     A2[k] = in ? a.A[(int64_t)(p.c0 + ch) * a.N + n] * LOG2E : 0.f;
-    h[k] = in && a.init ? a.init[((int64_t)p.b * a.C + p.c0 + ch) * a.N + n] : 0.f;
+    h[k] = in && from ? from[((int64_t)p.b * a.C + p.c0 + ch) * a.N + n] : 0.f;
   }
 }
 template <int NS, int CB, typename T>
-__device__ __forceinline__ void finish_state(const Args<T>& a, const Place<CB>& p, int ch, int q, const float (&h)[NS]) {
-  if (!a.final_state || ch >= p.nc) return;
+__device__ __forceinline__ void put_state(const Args<T>& a, const Place<CB>& p, int ch, int q, const float (&h)[NS],
+                                          float* to) {
+  if (!to || ch >= p.nc) return;
 #pragma unroll
   for (int k = 0; k < NS; ++k)
-    if (q * NS + k < a.N) a.final_state[((int64_t)p.b * a.C + p.c0 + ch) * a.N + q * NS + k] = h[k];
+    if (q * NS + k < a.N) to[((int64_t)p.b * a.C + p.c0 + ch) * a.N + q * NS + k] = h[k];
 }
 
 // ---------------------------------------------------------------- teams
@@ -286,40 +306,46 @@ struct Teams {
 // have been used and its sums are written.  Every thread of the block takes
 // part in each of them once per tile, waiting or only arriving.
 enum { FULL = 1, DONE = 3 };
+template <int THREADS>
 __device__ __forceinline__ void wait_for(int bar) {
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TEAM_THREADS) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(THREADS) : "memory");
 }
+template <int THREADS>
 __device__ __forceinline__ void arrive_at(int bar) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(bar), "n"(TEAM_THREADS) : "memory");
+  asm volatile("bar.arrive %0, %1;" ::"r"(bar), "n"(THREADS) : "memory");
 }
 
-template <typename T, int NS, int LPC, bool VEC, bool BVEC>
+// END: no outputs (and no output team), but what a segment adds to the state:
+// its end state from a zero start, and the sum of its steps, whose e^{A sum} is
+// what the segment leaves of the state that it begins with.
+template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool END>
 __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective_teams(const Args<T> a) {
+  constexpr int THREADS = END ? LANES + HELPERS : TEAM_THREADS;
   using S = Teams<T, NS, LPC, VEC, BVEC>;
   constexpr int CB = S::CB, NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
                 PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS, APART = S::APART, W = WORDS<T>;
   __shared__ __align__(16) float2 s_step[2][ROWS * CB];   // (s, s x)
   __shared__ __align__(16) uint32_t s_bc[2][ROWS * NP * W];  // (B, C)
-  __shared__ __align__(16) float s_y[2][TT * CB * PW];
+  __shared__ __align__(16) float s_y[2][END ? 4 : TT * CB * PW];
   __shared__ __align__(16) float s_D[CB], s_bias[CB];
   const Place<CB> p = place<CB>(a);
   const int tid = threadIdx.x, tiles = (int)(((int64_t)p.len + TT - 1) / TT);
-  for (int i = tid; i < CB; i += TEAM_THREADS) {
+  for (int i = tid; i < CB; i += THREADS) {
     s_D[i] = a.D && i < p.nc ? a.D[p.c0 + i] : 0.f;
     s_bias[i] = a.dt_bias && i < p.nc ? a.dt_bias[p.c0 + i] : 0.f;
   }
   __syncthreads();
 
-  if (tid >= LANES + HELPERS) {
+  if (!END && tid >= LANES + HELPERS) {
     // ---- output: add up the sums, skip and gate, store
     const int me = tid - LANES - HELPERS;
     const bool gate = a.z.p != nullptr;
-    for (int k = 0; k < 2 && k < tiles; ++k) arrive_at(FULL + k);
+    for (int k = 0; k < 2 && k < tiles; ++k) arrive_at<THREADS>(FULL + k);
     // piece k of a thread: token t0 + k * APART of the tile, channels c ..
     const int t0 = me / (CB / V), c = me % (CB / V) * V;
-    const T* px = a.x.row(p.b, t0) + p.c0 + c;
-    const T* pz = gate ? a.z.row(p.b, t0) + p.c0 + c : px;
-    T* py = a.y.row(p.b, t0) + p.c0 + c;
+    const T* px = a.x.row(p.b, p.t0 + t0) + p.c0 + c;
+    const T* pz = gate ? a.z.row(p.b, p.t0 + t0) + p.c0 + c : px;
+    T* py = a.y.row(p.b, p.t0 + t0) + p.c0 + c;
     Pack<T, V> nx[NX], nz[NX];
     auto fetch = [&](int left) {  // left: tokens of the sequence from this tile on
 #pragma unroll
@@ -341,7 +367,7 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
 #pragma unroll
       for (int k = 0; k < NX; ++k) x[k] = nx[k], z[k] = nz[k];
       if (tile + 1 < tiles) fetch(left - TT);
-      wait_for(DONE + k2);
+      wait_for<THREADS>(DONE + k2);
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
         const int t = t0 + k * APART;
@@ -358,7 +384,7 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
       }
       py += TT * a.y.ts;
       left -= TT;
-      if (tile + 2 < tiles) arrive_at(FULL + k2);
+      if (tile + 2 < tiles) arrive_at<THREADS>(FULL + k2);
     }
     return;
   }
@@ -367,10 +393,10 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
     // ---- operands: the step and the scaled input of every (token, channel), B and C
     const int me = tid - LANES;
     const int t0 = me / (CB / V), c = me % (CB / V) * V;
-    const T* px = a.x.row(p.b, t0) + p.c0 + c;
-    const T* pd = a.dt.row(p.b, t0) + p.c0 + c;
-    const T* pb = a.bm.row(p.b, 0) + (int64_t)p.g * a.N;
-    const T* pc = a.cm.row(p.b, 0) + (int64_t)p.g * a.N;
+    const T* px = a.x.row(p.b, p.t0 + t0) + p.c0 + c;
+    const T* pd = a.dt.row(p.b, p.t0 + t0) + p.c0 + c;
+    const T* pb = a.bm.row(p.b, p.t0) + (int64_t)p.g * a.N;
+    const T* pc = a.cm.row(p.b, p.t0) + (int64_t)p.g * a.N;
     Pack<T, V> nx[NX], nd[NX];
     Pack<T, VB> nb[NB], nc[NB];
     auto fetch = [&](int left) {
@@ -399,7 +425,7 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
 #pragma unroll 1
     for (int tile = 0; tile < tiles; ++tile) {
       const int k2 = tile & 1;
-      if (tile >= 2) wait_for(DONE + k2);
+      if (tile >= 2) wait_for<THREADS>(DONE + k2);
 #pragma unroll
       for (int k = 0; k < NX; ++k) {
         const int t = t0 + k * APART;
@@ -412,17 +438,18 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
         if (i < BP) put_bc<T, VB>(&s_bc[k2][i * VB * W], t < left && n < a.N, nb[k], nc[k]);
       }
       left -= TT;
-      arrive_at(FULL + k2);
+      arrive_at<THREADS>(FULL + k2);
       if (tile + 1 < tiles) fetch(left);
     }
-    for (int tile = tiles > 2 ? tiles - 2 : 0; tile < tiles; ++tile) arrive_at(DONE + (tile & 1));
+    for (int tile = tiles > 2 ? tiles - 2 : 0; tile < tiles; ++tile) arrive_at<THREADS>(DONE + (tile & 1));
     return;
   }
 
   // ---- the recurrence
   const int q = tid % LPC, ch = tid / LPC;
   float A2[NS], h[NS];
-  begin(a, p, ch, q, A2, h);
+  begin(a, p, ch, q, A2, h, END);
+  float steps = 0.f;  // END: the sum of the steps
   struct Operands {  // of U tokens
     float2 st[U];
     Entries<T, NS> bc[U];
@@ -449,6 +476,11 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
     float part[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) part[j] = advance<T, NS>(h, e[j], o.st[j].y, o.bc[j]);
+    if constexpr (END) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) steps += o.st[j].x;
+      return;
+    }
     if (DEFER && tg > 0) store(k2, tg - U);
 #pragma unroll
     for (int half = RED / 2; half > 0; half /= 2) {
@@ -470,7 +502,7 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
 #pragma unroll 1
   for (int tile = 0; tile < tiles; ++tile) {
     const int k2 = tile & 1;
-    wait_for(FULL + k2);
+    wait_for<THREADS>(FULL + k2);
     // Software pipeline over groups of U tokens: while group g is finished, the exponentials of g + 1 are under way
     // and the operands of g + 2 are loaded.
     Operands o[2];
@@ -487,10 +519,16 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
         read(k2, tg + (w + 2) * U, o[w]);
       }
     }
-    if (DEFER) store(k2, TT - U);
-    arrive_at(DONE + k2);
+    if (DEFER && !END) store(k2, TT - U);
+    arrive_at<THREADS>(DONE + k2);
   }
-  finish_state(a, p, ch, q, h);
+  if (END) {
+    const int64_t channels = a.B * a.C;
+    put_state(a, p, ch, q, h, a.starts + (p.seg + 1) * channels * a.N);
+    if (q == 0 && ch < p.nc) a.sums[p.seg * channels + (int64_t)p.b * a.C + p.c0 + ch] = steps;
+  } else if (p.seg + 1 == a.nseg) {
+    put_state(a, p, ch, q, h, a.final_state);
+  }
 }
 
 // ---------------------------------------------------------------- many
@@ -608,26 +646,108 @@ __global__ void __launch_bounds__(LANES, VEC && BVEC ? 5 : 4) k_selective_many(c
     }
     py += TT * a.y.ts;
   }
-  finish_state(a, p, ch, q, h);
+  put_state(a, p, ch, q, h, a.final_state);
+}
+
+// ---------------------------------------------------------------- segments
+//
+// The state that each segment begins with, in order: starts[k] arrives as the
+// end state of segment k - 1 from a zero start and leaves as
+//   starts[0] = init,  starts[k] += e^{A sums[k-1]} starts[k-1].
+// A state of 0 stays out of it: rates above 0 can make the factor infinite.
+template <typename T>
+__global__ void __launch_bounds__(256) k_selective_starts(const Args<T> a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, states = a.B * a.C * a.N;
+  if (i >= states) return;
+  const int64_t channel = i / a.N;
+  const float A2 = a.A[channel % a.C * a.N + i % a.N] * LOG2E;
+  float h = a.init ? a.init[i] : 0.f;
+  a.starts[i] = h;
+  // eight segments' loads under way together
+  constexpr int AT = 8;
+  for (int k = 1; k < a.nseg; k += AT) {
+    float sum[AT], end[AT];
+#pragma unroll
+    for (int j = 0; j < AT; ++j) {
+      const bool in = k + j < a.nseg;
+      sum[j] = in ? a.sums[(k + j - 1) * a.B * a.C + channel] : 0.f;
+      end[j] = in ? a.starts[(k + j) * states + i] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < AT; ++j) {
+      h = h == 0.f ? end[j] : fmaf(ex2(sum[j] * A2), h, end[j]);
+      if (k + j < a.nseg) a.starts[(k + j) * states + i] = h;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- choice
 
-template <typename T, int NS, int LPC>
+template <typename T, int NS, int LPC, bool END = false>
 cudaError_t launch_teams(Args<T> a, int64_t B, cudaStream_t st) {
   a.blocks_per_group = (uint32_t)ceil_div(a.per_group, LANES / LPC);
-  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group);
+  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group * (END ? a.nseg - 1 : a.nseg));
+  constexpr int threads = END ? LANES + HELPERS : TEAM_THREADS;
   if constexpr (NS * LPC % (16 / (int)sizeof(T)) == 0) {
     if (a.vec && a.bvec) {
-      k_selective_teams<T, NS, LPC, true, true><<<blocks, TEAM_THREADS, 0, st>>>(a);
+      k_selective_teams<T, NS, LPC, true, true, END><<<blocks, threads, 0, st>>>(a);
       return cudaGetLastError();
     }
   }
   if (a.vec)
-    k_selective_teams<T, NS, LPC, true, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
+    k_selective_teams<T, NS, LPC, true, false, END><<<blocks, threads, 0, st>>>(a);
   else
-    k_selective_teams<T, NS, LPC, false, false><<<blocks, TEAM_THREADS, 0, st>>>(a);
+    k_selective_teams<T, NS, LPC, false, false, END><<<blocks, threads, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+// A few channels leave most SMs idle, and a token takes the 16-lane kernel the
+// same time however few they are: a long sequence is cut into segments that run
+// at once, first for their end states, then, from the states that these give,
+// for the outputs.  That doubles the work, so it pays up to two thirds of the
+// SMs.  The count is the one of least estimated time among those that make one,
+// two or three blocks per SM, if that is at most 0.9 of the whole's; ns per token
+// as measured (bf16, rows on 16 bytes, all or but for B and C, or not; 4096 and
+// 16384 tokens).  Whole and cut:
+// 64 channels of 1024 tokens 23 and 11 us, of 16384 tokens 323 and 34, of 65536
+// tokens 1282 and 100; 384 of 4096 83 and 44, of 1024 23 and 18; 760 of 16384
+// 332 and 250; 1024 of 16384 346 and 356 (not taken).
+struct Rates {
+  double whole, per_sm[3];
+};
+inline int segments(const ssd_selective_dims* d, bool vec, bool bvec) {
+  if (d->dstate > 16 || d->seqlen <= 256) return 1;  // 256 tokens take 6 us: as long as the two launches more
+  static constexpr Rates ON_16{20, {19, 28, 32.5}}, X_ON_16{21.4, {27, 31.5, 1e9}}, APART{29, {35, 36, 1e9}};
+  const Rates& r = !vec ? APART : bvec ? ON_16 : X_ON_16;
+  const int64_t blocks = d->batch * d->ngroups * ceil_div(d->channels / d->ngroups, LANES / 16);
+  int best = 1;
+  double least = 0.9 * r.whole * d->seqlen;
+  for (int k = 0; k < 3; ++k) {
+    const int64_t n = std::min<int64_t>((k + 1) * 148 / blocks, MAX_SEGMENTS);
+    const double cut = 2 * r.per_sm[k] * ceil_div(d->seqlen, n < 1 ? 1 : n) + 5000 + 200 * n;
+    if (n >= 2 && cut <= least) least = cut, best = (int)n;
+  }
+  return best;
+}
+// starts (a multiple of 256 bytes) and sums of n segments, or 0
+inline size_t starts_bytes(const ssd_selective_dims* d, int n) {
+  return (size_t)ceil_div(n * d->batch * d->channels * d->dstate * 4, 256) * 256;
+}
+inline size_t segment_bytes(const ssd_selective_dims* d, int n) {
+  return n > 1 ? starts_bytes(d, n) + (size_t)(n - 1) * d->batch * d->channels * 4 : 0;
+}
+// for rows of any alignment
+inline size_t segment_bytes(const ssd_selective_dims* d) {
+  return segment_bytes(d, std::max({segments(d, true, true), segments(d, true, false), segments(d, false, false)}));
+}
+
+template <typename T>
+cudaError_t launch_segments(const Args<T>& a, int64_t B, cudaStream_t st) {
+  cudaError_t e = launch_teams<T, 1, 16, true>(a, B, st);
+  if (e != cudaSuccess) return e;
+  k_selective_starts<T><<<(unsigned)ceil_div(B * a.C * a.N, 256), 256, 0, st>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_teams<T, 1, 16>(a, B, st) : e;
 }
 
 template <typename T, int NS, int LPC>
@@ -644,12 +764,19 @@ cudaError_t launch_many(Args<T> a, int64_t B, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t launch_prompt(Args<T> a, int64_t B, cudaStream_t st) {
+cudaError_t launch_prompt(Args<T> a, int64_t B, const ssd_selective_dims* d, void* workspace, cudaStream_t st) {
   // rows on 16 bytes (vec, bvec as given) are moved in 16-byte pieces where groups of channels, and of states, are
   // whole pieces too
   constexpr int V = 16 / (int)sizeof(T);
   a.vec = a.vec && a.per_group % V == 0;
   a.bvec = a.bvec && a.N % V == 0;
+  if (workspace) {
+    a.nseg = segments(d, a.vec, a.bvec);
+    a.seg_len = ceil_div(a.L, a.nseg);
+    a.starts = static_cast<float*>(workspace);
+    a.sums = a.starts + starts_bytes(d, a.nseg) / sizeof(float);
+    if (a.nseg > 1) return launch_segments(a, B, st);
+  }
   // More lanes per channel make more warps of a small problem, at more instructions per channel, and teams help where
   // a scheduler has few warps.  The rule counts the recurrence's warps; the times are of 16 states, bf16, unless said
   // otherwise.  In a padded batch (lengths) sequences end early and it counts half of them (five sequences, three of

@@ -8,6 +8,7 @@ be loaded, importing a function raises -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -31,7 +32,7 @@ EXPORTED = ["ssd_status_string", "ssd_version", "ssd_scan_workspace_size", "ssd_
             "ssd_scan_fwd_strided", "ssd_selftest_carry_timeout", "ssd_scan_fwd_vdecay",
             "ssd_selftest_set_segments", "ssd_selftest_set_split", "ssd_selftest_set_step_chunks",
             "ssd_scan_fwd_normed", "ssd_conv_fwd", "ssd_conv_step", "ssd_selective_fwd", "ssd_selective_step",
-            "ssd_rmsnorm_gated"]
+            "ssd_rmsnorm_gated", "ssd_selective_workspace_size"]
 
 
 class SSDError(RuntimeError):
@@ -113,7 +114,9 @@ def lib() -> ctypes.CDLL:
         "ssd_conv_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _P]),
         "ssd_conv_step": (ctypes.c_int, [_P, _P, _I64, _P, _P, _P, _P, _I64, _P]),
         "ssd_selective_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P,
-                                             _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+                                             _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P,
+                                             ctypes.c_size_t, _P]),
+        "ssd_selective_workspace_size": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
         "ssd_selective_step": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P,
                                               _I64, _P]),
         "ssd_rmsnorm_gated": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I64,
@@ -419,7 +422,7 @@ def ssd_step(x, dt, A, Bm, Cm, state, D=None, y=None, stream=None, input_dt: boo
 # ---- the layer around and beside the scan -------------------------------------------------
 #
 # A single token is a few microseconds of GPU time, so these bindings look at each tensor once: the checks hand back
-# what the call takes (address and strides).
+# what the call takes (address and strides).  Forward only: no gradient is recorded.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -502,10 +505,22 @@ def _call(name: str, dev: int, stream, *args):
         _check(s, name)
 
 
-def _new_rows(x: torch.Tensor, lengths=None):
+def _on(stream, device):
+    """torch's work on the stream that a call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _new_rows(x: torch.Tensor, lengths=None, stream=None):
+    if lengths is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     # rows behind a padded sequence are not written: zeros there, not what memory held
-    make = torch.empty_like if lengths is None else torch.zeros_like
-    return make(x, memory_format=torch.contiguous_format)
+    with _on(stream, x.device):
+        return torch.zeros_like(x, memory_format=torch.contiguous_format)
 
 
 _NONE2, _NONE1 = (0, 0), (0,)
@@ -525,7 +540,7 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, lengths=None, silu: bool
     W = weight.shape[1]
     dev, io, f32 = _device_of(x), x.dtype, torch.float32
     if y is None:
-        y = _new_rows(x, lengths)
+        y = _new_rows(x, lengths, stream)
     if final_state is None and want_final:
         final_state = torch.empty((Bz, max(W - 1, 0), C), dtype=io, device=x.device)
     dims = ConvDims(Bz, L, C, W, _io(x), int(silu))
@@ -554,13 +569,23 @@ def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream
     return y
 
 
+def ssd_selective_workspace_size(dims: SelectiveDims) -> int:
+    n = ctypes.c_size_t(0)
+    s = (_lib or lib()).ssd_selective_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if s != 0:
+        _check(s, "ssd_selective_workspace_size")
+    return n.value
+
+
 def ssd_selective_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state=None, lengths=None,
-                      softplus: bool = True, y=None, final_state=None, stream=None, want_final: bool = True):
+                      softplus: bool = True, y=None, final_state=None, workspace=None, stream=None,
+                      want_final: bool = True):
     """The selective scan with a step per channel: x, dt, z [B,L,C], Bm, Cm [B,L,G,N] (any batch and token
     strides, one pair for Bm and Cm), A [C,N], D, dt_bias [C] f32; the step is softplus(dt + dt_bias)
     (softplus=False: dt + dt_bias), y is gated by silu(z) where z is given.  init_state [B,C,N] f32
     (None: zeros), lengths [B] int32 as in ssd_conv_fwd.  Returns (y, final_state [B,C,N] or None);
-    final_state may be init_state itself."""
+    final_state may be init_state itself.  workspace: a tensor of at least ssd_selective_workspace_size
+    bytes (made here where that is not 0)."""
     shape = x.shape
     if len(shape) != 3:
         raise SSDError(2, "x must be [B,L,C]")
@@ -568,15 +593,24 @@ def ssd_selective_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, init_state
     dev, io, f32 = _device_of(x), x.dtype, torch.float32
     G, N, at_b, at_c, bc = _groups(x, Bm, Cm, dev)
     if y is None:
-        y = _new_rows(x, lengths)
+        y = _new_rows(x, lengths, stream)
     if final_state is None and want_final:
         final_state = torch.empty((Bz, C, N), dtype=f32, device=x.device)
     dims = SelectiveDims(Bz, L, C, N, G, _io(x), int(softplus))
+    if workspace is None:
+        nbytes = 0 if L <= 256 else ssd_selective_workspace_size(dims)
+        if nbytes:
+            with _on(stream, x.device):  # given back on return: of the stream that uses it
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SSDError(1, "the workspace must be contiguous and on the tensors' device")
+    at_ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                           workspace.numel() * workspace.element_size())
     _call("ssd_selective_fwd", dev, stream, ctypes.byref(dims), *_rows(x, shape, io, dev, _NONE2),
           *_rows(dt, shape, io, dev, _NONE2), _whole(A, (C, N), f32, dev), at_b, at_c, *bc, _whole(D, (C,), f32, dev),
           *_rows(z, shape, io, dev, _NONE2), _whole(dt_bias, (C,), f32, dev),
           _whole(init_state, (Bz, C, N), f32, dev), _whole(lengths, (Bz,), torch.int32, dev),
-          *_rows(y, shape, io, dev, _NONE2), _whole(final_state, (Bz, C, N), f32, dev))
+          *_rows(y, shape, io, dev, _NONE2), _whole(final_state, (Bz, C, N), f32, dev), at_ws, ws_bytes)
     return y, final_state
 
 

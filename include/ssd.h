@@ -418,8 +418,10 @@ ssd_status ssd_scan_fwd_vdecay(const ssd_dims* d, const void* x, const float* dt
  *    state).
  *  - Outputs must not overlap inputs (SSD_ERR_INVALID_ARG), but for
  *    final_state, which may be init_state itself: a cache updated in place.
- *  - No workspace, nothing kept between calls, one launch per call: every call
- *    can be captured into a CUDA graph.
+ *  - Nothing is kept between calls and nothing is waited for on the host: every
+ *    call can be captured into a CUDA graph.  One launch and no workspace, but for
+ *    the segments of ssd_selective_fwd.
+ *  - Forward only: no gradients.
  */
 
 /* SSD_CONV_SILU: y = silu(.) instead of the convolution's sum itself. */
@@ -478,6 +480,15 @@ typedef struct ssd_selective_dims {
 } ssd_selective_dims;
 
 /*
+ * Bytes of device workspace with which ssd_selective_fwd runs `d` in segments:
+ * a long sequence of few channels, which would leave most SMs idle, is cut into
+ * up to 64 segments that run at once (three launches: their end states, the
+ * states that they begin with, their outputs).  0 where the whole sequences are
+ * as fast, as they are up to 256 tokens.
+ */
+ssd_status ssd_selective_workspace_size(const ssd_selective_dims* d, size_t* bytes);
+
+/*
  * The selective scan with a step of its own for every channel and a decay rate
  * for every state entry -- the diagonal state matrix of
  * "告别Transformer的二次方噩梦：用Mamba（S6）模型在长文本任务中实现线性时间推理" §2.1, with
@@ -491,14 +502,16 @@ typedef struct ssd_selective_dims {
  *   x, dt, z, y: rows of C channels (z may be NULL); A [C,N] f32, D, dt_bias
  *   [C] f32 or NULL (= 0);
  *   Bm, Cm: rows of G*N entries with one pair of strides for both;
- *   init_state, final_state [B,C,N] f32 or NULL.
+ *   init_state, final_state [B,C,N] f32 or NULL;
+ *   workspace: device scratch of at least ssd_selective_workspace_size bytes,
+ *   16-byte aligned, or NULL for whole sequences (the same results up to rounding).
  */
 ssd_status ssd_selective_fwd(const ssd_selective_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
                              const void* dt, int64_t dt_bstride, int64_t dt_tstride, const float* A, const void* Bm,
                              const void* Cm, int64_t bc_bstride, int64_t bc_tstride, const float* D, const void* z,
                              int64_t z_bstride, int64_t z_tstride, const float* dt_bias, const float* init_state,
                              const int32_t* lengths, void* y, int64_t y_bstride, int64_t y_tstride,
-                             float* final_state, void* stream);
+                             float* final_state, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * One token of it: x, dt, z, y [B,C], Bm, Cm [B,G,N] (rows *_bstride apart),

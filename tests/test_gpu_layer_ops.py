@@ -293,6 +293,117 @@ def test_selective_in_pieces_is_the_whole():
     close(cache, state, sbound, "f32")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,C,N,G,pad,lengths", [
+    (1, 2000, 64, 16, 1, (8, 0), None),
+    (1, 1500, 30, 13, 3, (1, 0), None),
+    (3, 1301, 65, 16, 1, (0, 0), [1301, 0, 640]),
+    (2, 1024, 40, 3, 1, (0, 2), [1, 1024]),
+    (4, 900, 32, 16, 1, (0, 0), None),
+])
+def test_selective_in_segments(io, B, L, C, N, G, pad, lengths):
+    """Long sequences of few channels: cut into segments, as one, and in place."""
+    d = scan_inputs(io, B, L, C, N, G, seed=75, bias=-4.0, pad=pad)
+    dims = ssd.SelectiveDims(B, L, C, N, G, int(io == "bf16"), 1)
+    size = ssd.ssd_selective_workspace_size(dims)
+    assert size > 0
+    st = rnd(76, B, C, N)
+    if lengths is not None:
+        for k, n in enumerate(lengths):
+            for name in ("x", "dt", "z", "Bm", "Cm"):
+                d[name][k, n:] = float("nan")
+    want, bound, state, sbound = scan_want(d, st, lengths)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # NaN: nothing is read before it is written
+    y = torch.full((B, L, C), 7.0, dtype=IO[io], device="cuda")
+    cache = st.clone()
+    got, fin = ssd.ssd_selective_fwd(**d, init_state=cache, final_state=cache, lengths=lens(lengths), y=y, workspace=ws)
+    assert fin is cache
+    for k in range(B):
+        m = L if lengths is None else lengths[k]
+        close(got[k, :m], want[k, :m], bound[k, :m], io)
+        assert torch.all(got[k, m:] == 7.0)
+    close(cache, state, sbound, "f32")
+    again, last = ssd.ssd_selective_fwd(**d, init_state=st, lengths=lens(lengths))
+    for k in range(B):
+        m = L if lengths is None else lengths[k]
+        assert torch.equal(again[k, :m], got[k, :m])
+    assert torch.equal(last, cache)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    there = [ssd.ssd_selective_fwd(**d, init_state=st, lengths=lens(lengths), stream=s)
+             for s in (side, side.cuda_stream)]
+    side.synchronize()
+    assert all(torch.equal(f, cache) for _, f in there)
+    zero, _ = ssd.ssd_selective_fwd(**d, lengths=lens(lengths), want_final=False)
+    want, bound, _, _ = scan_want(d, None, lengths)
+    for k in range(B):
+        m = L if lengths is None else lengths[k]
+        close(zero[k, :m], want[k, :m], bound[k, :m], io)
+
+
+def test_selective_in_segments_with_growing_states():
+    """Rates above 0: a segment's factor is infinite while the state is still 0, which it then stays."""
+    d = scan_inputs("f32", 1, 2000, 16, 16, 1, seed=78)
+    d["A"] = torch.full_like(d["A"], 4.0)
+    d["dt_bias"] = torch.zeros_like(d["dt_bias"])
+    d["dt"][:, :1000], d["dt"][:, 1000:] = 1.0, -12.0
+    d["x"][:, :1000] = 0.0
+    assert ssd.ssd_selective_workspace_size(ssd.SelectiveDims(1, 2000, 16, 16, 1, 0, 1)) > 0
+    want, bound, state, sbound = scan_want(d, None, None)
+    got, fin = ssd.ssd_selective_fwd(**d)
+    close(got, want, bound, "f32")
+    close(fin, state, sbound, "f32")
+
+
+def test_zeros_behind_sequences_on_another_stream():
+    """A y made for a padded batch is filled on the stream that then writes it, not behind it on the current one."""
+    d = scan_inputs("bf16", 2, 300, 64, 16, 1, seed=79)
+    ln = lens([300, 120])
+    w, b = rnd(81, 64, 4), rnd(82, 64)
+    want = ssd.ssd_selective_fwd(**d, lengths=ln)[0], ssd.ssd_conv_fwd(d["x"], w, b, lengths=ln)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second of the current stream
+        got = [ssd.ssd_selective_fwd(**d, lengths=ln, stream=s)[0], ssd.ssd_conv_fwd(d["x"], w, b, lengths=ln, stream=s)[0]]
+        torch.cuda.synchronize()
+        for g, y in zip(got, want):
+            assert torch.equal(g, y)
+
+
+def test_selective_refuses_workspaces():
+    d = scan_inputs("bf16", 1, 2000, 64, 16, 1, seed=83)
+    size = ssd.ssd_selective_workspace_size(ssd.SelectiveDims(1, 2000, 64, 16, 1, 1, 1))
+    byte = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for ws in (byte.expand(size), byte, torch.zeros(size), torch.zeros(size + 8, dtype=torch.uint8, device="cuda")[8:]):
+        with pytest.raises(ssd.SSDError):
+            ssd.ssd_selective_fwd(**d, workspace=ws)
+
+
+def test_selective_in_segments_captured():
+    """Its launches and workspace inside a graph: two graphs, replayed in turn, keep to their own."""
+    graphs, held, ins, outs = [], [], [], []
+    for seed in (77, 87):
+        d = scan_inputs("bf16", 1, 1200, 48, 16, 1, seed=seed)
+        ssd.ssd_selective_fwd(**d)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(ssd.ssd_selective_fwd(**d))
+        graphs.append(g)
+        ins.append(d)
+    for k in range(2):
+        for i in range(2):
+            ins[i]["x"].copy_(rnd(97 + 2 * k + i, *ins[i]["x"].shape, io="bf16"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for d, (y, fin) in zip(ins, held):
+            want, last = ssd.ssd_selective_fwd(**d)
+            assert torch.equal(y, want) and torch.equal(fin, last)
+    del graphs
+
+
 def test_selective_with_one_rate_is_the_vector_decay_scan():
     """With x scaled by the step, one channel per head and N rates: ssd_scan_fwd_vdecay at head dim 1."""
     d = scan_inputs("f32", 2, 50, 12, 16, 2, seed=80, gate=False)

@@ -60,7 +60,8 @@ def scan(lib, **o):
     return lib.ssd_selective_fwd(ctypes.byref(dims), g("x", at(0)), 6400, g("xt", 64), g("dt", at(1)), 6400, 64,
                                  g("A", at(2)), g("B", at(3)), g("C", at(4)), 1600, g("bct", 16), g("D", at(5)),
                                  g("z", at(6)), 6400, 64, g("bias", at(7)), g("init", at(8)), g("lengths", at(9)),
-                                 g("y", at(10)), 6400, g("yt", 64), g("final", at(11)), None)
+                                 g("y", at(10)), 6400, g("yt", 64), g("final", at(11)),
+                                 g("ws", None), g("wsb", 0), None)
 
 
 @pytest.mark.parametrize("o,status", [
@@ -70,7 +71,14 @@ def scan(lib, **o):
     (dict(x=None), 1), (dict(dt=None), 1), (dict(A=None), 1), (dict(B=None), 1), (dict(C=None), 1), (dict(y=None), 1),
     (dict(dt=at(1, 1)), 4), (dict(A=at(2, 2)), 4), (dict(final=at(11, 2)), 4), (dict(xt=-1), 2), (dict(bct=-16), 2),
     (dict(yt=60), 2), (dict(y=at(0)), 1), (dict(y=at(6, 64)), 1), (dict(y=at(3)), 1), (dict(final=at(8, 64)), 1),
-    (dict(final=at(2)), 1), (dict(final=at(10)), 1), (dict(y=at(8)), 1),
+    (dict(final=at(2)), 1), (dict(final=at(10)), 1), (dict(y=at(8)), 1), (dict(ws=at(12, 8)), 4),
+    (dict(batch=1, seqlen=4096, ws=at(12), wsb=1024), 6),
+    (dict(batch=1, seqlen=4096, ws=at(0), wsb=1 << 20), 1),
+    (dict(batch=1, seqlen=4096, ws=at(2), wsb=1 << 20), 1),
+    (dict(batch=1, seqlen=4096, ws=at(9), wsb=1 << 20), 1),
+    (dict(batch=1, seqlen=4096, ws=at(8), wsb=1 << 20), 1),
+    (dict(batch=1, seqlen=4096, ws=at(10), wsb=1 << 20), 1),
+    (dict(batch=1, seqlen=4096, ws=at(11), wsb=1 << 20), 1),
 ])
 def test_selective_refuses(lib, o, status):
     assert scan(lib, **o) == status, ssd.status_string(scan(lib, **o))
@@ -109,3 +117,26 @@ def test_the_binding_takes_no_host_tensors():
         with pytest.raises(ssd.SSDError) as e:
             call()
         assert e.value.status == 1
+
+
+def test_selective_workspace(lib):
+    """Segments where they pay: few channels, long sequences, up to 16 states."""
+    def size(**o):
+        names = dict(batch=1, seqlen=4096, channels=64, dstate=16, ngroups=1, io=1, flags=1)
+        n = ctypes.c_size_t(7)
+        d = ssd.SelectiveDims(*(o.get(k, v) for k, v in names.items()))
+        return lib.ssd_selective_workspace_size(ctypes.byref(d), ctypes.byref(n)), n.value
+
+    def bytes_of(n, channels, N=16):
+        return -(-n * channels * N * 4 // 256) * 256 + (n - 1) * channels * 4
+
+    # 8 blocks of 8 channels: 37 segments make two blocks for each of 148 SMs, 55 three
+    assert size() == (0, bytes_of(37, 64))
+    assert size(seqlen=512)[1] >= bytes_of(18, 64) and size(seqlen=1 << 20)[1] == bytes_of(55, 64)
+    assert size(channels=1, dstate=1, seqlen=1 << 30)[1] == bytes_of(64, 1, 1)
+    assert size(channels=384)[1] == bytes_of(9, 384)
+    assert size(channels=2048) == (0, 0) and size(batch=32) == (0, 0)   # the SMs are taken already
+    assert size(seqlen=200) == (0, 0) and size(dstate=17) == (0, 0)
+    assert size(dstate=0)[0] == 2 and size(dstate=129)[0] == 5
+    assert lib.ssd_selective_workspace_size(None, ctypes.byref(ctypes.c_size_t())) == 1
+    assert lib.ssd_selective_workspace_size(ctypes.byref(ssd.SelectiveDims(1, 1, 1, 1, 1, 1, 0)), None) == 1
