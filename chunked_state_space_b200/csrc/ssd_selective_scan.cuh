@@ -36,7 +36,7 @@ namespace selective {
 constexpr int LANES = 128;  // lanes of a block that carry the recurrence
 constexpr int HELPERS = 64, TEAM_THREADS = LANES + 2 * HELPERS;
 constexpr int64_t SCHEDULERS = 4 * 148;  // warp schedulers of the GPU
-constexpr int MAX_SEGMENTS = 64;
+constexpr int MAX_SEGMENTS = 128;
 
 template <typename T>
 struct Args {
@@ -50,11 +50,11 @@ struct Args {
   int C, N, G, per_group;
   uint32_t blocks_per_group, total;
   bool softplus, vec, bvec;
-  // Segments of seg_len tokens of every sequence (1: the whole sequences).  With more than one, starts [nseg,B,C,N]
-  // holds the state that each begins with, sums [nseg - 1,B,C] the steps that it takes in all.
-  int nseg;
+  // Segments of seg_len tokens of every sequence (1: the whole sequences), the first of this launch; with more than
+  // one, the end states [nseg - 1,B,C,N] and the sums of steps [nseg - 1,B,C] of all but the last.
+  int nseg, seg0;
   int64_t seg_len;
-  float *starts, *sums;
+  float *ends, *sums;
 };
 
 // max(v, 0) + log1p(e^-|v|); |v| beyond 128, infinite or the type's lowest, counts
@@ -244,7 +244,7 @@ __device__ __forceinline__ Place<CB> place(const Args<T>& a) {
   p.g = r % (uint32_t)a.G;
   r /= (uint32_t)a.G;
   p.b = a.nseg == 1 ? r : r % (uint32_t)a.B;
-  p.seg = a.nseg == 1 ? 0 : r / (uint32_t)a.B;
+  p.seg = a.nseg == 1 ? 0 : r / (uint32_t)a.B + a.seg0;
   p.c0 = (int)p.g * a.per_group + (int)cb * CB;
   p.nc = min(CB, ((int)p.g + 1) * a.per_group - p.c0);
   p.t0 = p.seg * a.seg_len;
@@ -253,9 +253,8 @@ __device__ __forceinline__ Place<CB> place(const Args<T>& a) {
   return p;
 }
 template <int NS, int CB, typename T>
-__device__ __forceinline__ void begin(const Args<T>& a, const Place<CB>& p, int ch, int q, float (&A2)[NS], float (&h)[NS],
-                                      bool from_zero = false) {
-  const float* from = from_zero ? nullptr : a.nseg == 1 ? a.init : a.starts + (int64_t)p.seg * a.B * a.C * a.N;
+__device__ __forceinline__ void begin(const Args<T>& a, const Place<CB>& p, int ch, int q, const float* from,
+                                      float (&A2)[NS], float (&h)[NS]) {
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const int n = q * NS + k;
@@ -271,6 +270,45 @@ __device__ __forceinline__ void put_state(const Args<T>& a, const Place<CB>& p, 
 #pragma unroll
   for (int k = 0; k < NS; ++k)
     if (q * NS + k < a.N) to[((int64_t)p.b * a.C + p.c0 + ch) * a.N + q * NS + k] = h[k];
+}
+
+// The state that segment p.seg, not the first, begins with, from h, the end
+// state of the first: h = e^{A sum} h + end, segment by segment.  A state of 0
+// stays out of it: rates above 0 can make the factor infinite.
+template <int NS, int CB, typename T>
+__device__ __forceinline__ void through_segments(const Args<T>& a, const Place<CB>& p, int ch, int q,
+                                                 const float (&A2)[NS], float (&h)[NS]) {
+  if (ch >= p.nc) return;
+  const int64_t channels = a.B * a.C, at = (int64_t)p.b * a.C + p.c0 + ch;
+  const float *ends = a.ends + at * a.N + q * NS, *sums = a.sums + at;
+  constexpr int AHEAD = NS > 2 ? 4 : 8;  // segments whose loads are under way together
+  for (int k = 1; k < (int)p.seg; k += AHEAD) {
+    float sum[AHEAD], end[AHEAD][NS];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const bool in = k + j < (int)p.seg;
+      sum[j] = in ? sums[(k + j) * channels] : 0.f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) end[j][n] = in && q * NS + n < a.N ? ends[(k + j) * channels * a.N + n] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n) h[n] = h[n] == 0.f ? end[j][n] : fmaf(ex2(sum[j] * A2[n]), h[n], end[j][n]);
+    }
+  }
+}
+// What a block leaves in the workspace or as the final state.
+template <bool END, int NS, int CB, typename T>
+__device__ __forceinline__ void leave(const Args<T>& a, const Place<CB>& p, int ch, int q, const float (&h)[NS],
+                                      float steps) {
+  const int64_t channels = a.B * a.C;
+  if constexpr (END) {
+    put_state(a, p, ch, q, h, a.ends + p.seg * channels * a.N);
+    if (q == 0 && ch < p.nc) a.sums[p.seg * channels + (int64_t)p.b * a.C + p.c0 + ch] = steps;
+  } else {
+    put_state(a, p, ch, q, h, p.seg + 1 == a.nseg ? a.final_state : p.seg == 0 ? a.ends : nullptr);
+  }
 }
 
 // ---------------------------------------------------------------- teams
@@ -315,28 +353,31 @@ __device__ __forceinline__ void arrive_at(int bar) {
   asm volatile("bar.arrive %0, %1;" ::"r"(bar), "n"(THREADS) : "memory");
 }
 
+template <typename S, int W>
+struct TeamsShared {
+  __align__(16) float2 step[2][S::ROWS * S::CB];        // (s, s x)
+  __align__(16) uint32_t bc[2][S::ROWS * S::NP * W];    // (B, C)
+  __align__(16) float y[2][S::TT * S::CB * S::PW];
+  __align__(16) float D[S::CB], bias[S::CB];
+};
+
 // END: no outputs (and no output team), but what a segment adds to the state:
 // its end state from a zero start, and the sum of its steps, whose e^{A sum} is
 // what the segment leaves of the state that it begins with.
-template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool END>
-__global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective_teams(const Args<T> a) {
+template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool END, typename Shared, int CB>
+__device__ __forceinline__ void run_teams(const Args<T>& a, const Place<CB>& p, Shared& sh) {
   constexpr int THREADS = END ? LANES + HELPERS : TEAM_THREADS;
   using S = Teams<T, NS, LPC, VEC, BVEC>;
-  constexpr int CB = S::CB, NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
-                PW = S::PW, RED = S::RED, U = S::U, ROWS = S::ROWS, APART = S::APART, W = WORDS<T>;
-  __shared__ __align__(16) float2 s_step[2][ROWS * CB];   // (s, s x)
-  __shared__ __align__(16) uint32_t s_bc[2][ROWS * NP * W];  // (B, C)
-  __shared__ __align__(16) float s_y[2][END ? 4 : TT * CB * PW];
-  __shared__ __align__(16) float s_D[CB], s_bias[CB];
-  const Place<CB> p = place<CB>(a);
+  constexpr int NP = S::NP, V = S::V, VB = S::VB, TT = S::TT, XP = S::XP, BP = S::BP, NX = S::NX, NB = S::NB,
+                PW = S::PW, RED = S::RED, U = S::U, APART = S::APART, W = WORDS<T>;
+  auto& s_step = sh.step;
+  auto& s_bc = sh.bc;
+  auto& s_y = sh.y;
+  auto& s_D = sh.D;
+  auto& s_bias = sh.bias;
   const int tid = threadIdx.x, tiles = (int)(((int64_t)p.len + TT - 1) / TT);
-  for (int i = tid; i < CB; i += THREADS) {
-    s_D[i] = a.D && i < p.nc ? a.D[p.c0 + i] : 0.f;
-    s_bias[i] = a.dt_bias && i < p.nc ? a.dt_bias[p.c0 + i] : 0.f;
-  }
-  __syncthreads();
-
-  if (!END && tid >= LANES + HELPERS) {
+  if (tid >= LANES + HELPERS) {
+    if constexpr (END) return;
     // ---- output: add up the sums, skip and gate, store
     const int me = tid - LANES - HELPERS;
     const bool gate = a.z.p != nullptr;
@@ -448,7 +489,10 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
   // ---- the recurrence
   const int q = tid % LPC, ch = tid / LPC;
   float A2[NS], h[NS];
-  begin(a, p, ch, q, A2, h, END);
+  begin(a, p, ch, q, END ? nullptr : p.seg == 0 ? a.init : a.ends, A2, h);
+  if constexpr (!END) {
+    if (p.seg > 1) through_segments(a, p, ch, q, A2, h);
+  }
   float steps = 0.f;  // END: the sum of the steps
   struct Operands {  // of U tokens
     float2 st[U];
@@ -522,47 +566,77 @@ __global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 
     if (DEFER && !END) store(k2, TT - U);
     arrive_at<THREADS>(DONE + k2);
   }
-  if (END) {
-    const int64_t channels = a.B * a.C;
-    put_state(a, p, ch, q, h, a.starts + (p.seg + 1) * channels * a.N);
-    if (q == 0 && ch < p.nc) a.sums[p.seg * channels + (int64_t)p.b * a.C + p.c0 + ch] = steps;
-  } else if (p.seg + 1 == a.nseg) {
-    put_state(a, p, ch, q, h, a.final_state);
+  leave<END>(a, p, ch, q, h, steps);
+}
+
+// MIXED: of all segments but the last, the outputs of the first and the END of
+// the others; otherwise the outputs of all of them.
+template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool MIXED>
+__global__ void __launch_bounds__(TEAM_THREADS, NS * LPC <= 16 && VEC && BVEC ? 3 : 2) k_selective_teams(const Args<T> a) {
+  using S = Teams<T, NS, LPC, VEC, BVEC>;
+  __shared__ TeamsShared<S, WORDS<T>> sh;
+  const Place<S::CB> p = place<S::CB>(a);
+  for (int i = threadIdx.x; i < S::CB; i += TEAM_THREADS) {
+    sh.D[i] = a.D && i < p.nc ? a.D[p.c0 + i] : 0.f;
+    sh.bias[i] = a.dt_bias && i < p.nc ? a.dt_bias[p.c0 + i] : 0.f;
   }
+  __syncthreads();
+  if (MIXED && p.seg > 0)
+    run_teams<T, NS, LPC, VEC, BVEC, true>(a, p, sh);
+  else
+    run_teams<T, NS, LPC, VEC, BVEC, false>(a, p, sh);
 }
 
 // ---------------------------------------------------------------- many
 
-template <typename T, int NS, int LPC, bool VEC, bool BVEC>
-__global__ void __launch_bounds__(LANES, VEC && BVEC ? 5 : 4) k_selective_many(const Args<T> a) {
-  constexpr int CB = LANES / LPC, NP = NS * LPC, TT = 8 * LPC;  // eight elements of x per thread and tile
+template <typename T, int NS, int LPC>
+struct Many {
+  static constexpr int CB = LANES / LPC, NP = NS * LPC, TT = 8 * LPC;  // eight elements of x per thread and tile
+  static constexpr int YS = CB + (LPC == 4 ? 8 : 4);  // a row of sums: a warp writes 32 / LPC channels of LPC tokens
+};
+template <typename S, int W>
+struct ManyShared {
+  __align__(16) float2 step[S::TT * S::CB];        // (s, s x)
+  __align__(16) uint32_t bc[S::TT * S::NP * W];  // (B, C)
+  __align__(16) float y[S::TT * S::YS];
+  __align__(16) float D[S::CB], bias[S::CB];
+};
+
+// END as in run_teams: no outputs, z and C are not read.
+template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool END, typename Shared, int CB>
+__device__ __forceinline__ void run_many(const Args<T>& a, const Place<CB>& p, Shared& sh) {
+  using S = Many<T, NS, LPC>;
+  constexpr int NP = S::NP, TT = S::TT, YS = S::YS;
   constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, VB = BVEC ? 16 / (int)sizeof(T) : 1, W = WORDS<T>;
   constexpr int NX = 8 / V, BP = TT * NP / VB, NB = (BP + LANES - 1) / LANES, APART = LANES / (CB / V);
   constexpr int U = 8;           // tokens whose sums are exchanged together: a lane ends up with U / LPC of them
   constexpr int KEEP = U / LPC;
-  constexpr int YS = CB + (LPC == 4 ? 8 : 4);  // a row of sums: a warp writes 32 / LPC channels of LPC tokens
   static_assert(NP % VB == 0 && CB % V == 0 && U % LPC == 0 && TT % U == 0, "rows and tiles are whole pieces");
-  __shared__ __align__(16) float2 s_step[TT * CB];     // (s, s x)
-  __shared__ __align__(16) uint32_t s_bc[TT * NP * W];  // (B, C)
-  __shared__ __align__(16) float s_y[TT * YS];
-  __shared__ __align__(16) float s_D[CB], s_bias[CB];
-  const Place<CB> p = place<CB>(a);
+  auto& s_step = sh.step;
+  auto& s_bc = sh.bc;
+  auto& s_y = sh.y;
+  auto& s_D = sh.D;
+  auto& s_bias = sh.bias;
   const int tid = threadIdx.x, q = tid % LPC, ch = tid / LPC;
   float A2[NS], h[NS];
-  begin(a, p, ch, q, A2, h);
+  begin(a, p, ch, q, END ? nullptr : p.seg == 0 ? a.init : a.ends, A2, h);
+  if constexpr (!END) {
+    if (p.seg > 1) through_segments(a, p, ch, q, A2, h);
+  }
+  float steps = 0.f;  // END: the sum of the steps
   for (int i = tid; i < CB; i += LANES) {
     s_D[i] = a.D && i < p.nc ? a.D[p.c0 + i] : 0.f;
     s_bias[i] = a.dt_bias && i < p.nc ? a.dt_bias[p.c0 + i] : 0.f;
   }
-  const bool gate = a.z.p != nullptr;
+  const bool gate = !END && a.z.p != nullptr;
   // piece k of a thread: token t0 + k * APART of the tile, channels c ..
   const int t0 = tid / (CB / V), c = tid % (CB / V) * V;
-  const T* px = a.x.row(p.b, t0) + p.c0 + c;
-  const T* pd = a.dt.row(p.b, t0) + p.c0 + c;
-  const T* pz = gate ? a.z.row(p.b, t0) + p.c0 + c : px;
-  T* py = a.y.row(p.b, t0) + p.c0 + c;
-  const T* pb = a.bm.row(p.b, 0) + (int64_t)p.g * a.N;
-  const T* pc = a.cm.row(p.b, 0) + (int64_t)p.g * a.N;
+  const T* px = a.x.row(p.b, p.t0 + t0) + p.c0 + c;
+  const T* pd = a.dt.row(p.b, p.t0 + t0) + p.c0 + c;
+  const T* pz = gate ? a.z.row(p.b, p.t0 + t0) + p.c0 + c : px;
+  T* py = a.y.row(p.b, p.t0 + t0) + p.c0 + c;
+  const T* pb = a.bm.row(p.b, p.t0) + (int64_t)p.g * a.N;
+  const T* pc = a.cm.row(p.b, p.t0) + (int64_t)p.g * a.N;
   Pack<T, V> nx[NX], nd[NX], nz[NX];
   Pack<T, VB> nb[NB], nc[NB];
   auto fetch = [&](int left) {
@@ -579,7 +653,7 @@ __global__ void __launch_bounds__(LANES, VEC && BVEC ? 5 : 4) k_selective_many(c
       const int i = tid + k * LANES, t = i / (NP / VB), n = i % (NP / VB) * VB;
       if (i < BP && t < left && n < a.N) {
         nb[k] = load_pack<T, VB>(pb + t * a.bm.ts + n);
-        nc[k] = load_pack<T, VB>(pc + t * a.cm.ts + n);
+        nc[k] = END ? nb[k] : load_pack<T, VB>(pc + t * a.cm.ts + n);
       }
     }
     px += TT * a.x.ts;
@@ -618,149 +692,210 @@ __global__ void __launch_bounds__(LANES, VEC && BVEC ? 5 : 4) k_selective_many(c
         float e[NS];
         decays<NS>(st.x, A2, e);
         part[j] = advance<T, NS>(h, e, st.y, bc);
+        if (END) steps += st.x;
       }
-      // the LPC parts of every sum: each exchange halves the tokens that a lane still holds
+      if constexpr (!END) {
+        // the LPC parts of every sum: each exchange halves the tokens that a lane still holds
 #pragma unroll
-      for (int half = LPC / 2; half > 0; half /= 2) {
-        const bool up = (q & half) != 0;
+        for (int half = LPC / 2; half > 0; half /= 2) {
+          const bool up = (q & half) != 0;
 #pragma unroll
-        for (int j = 0; j < half * KEEP; ++j) {
-          const float give = up ? part[j] : part[j + half * KEEP], keep = up ? part[j + half * KEEP] : part[j];
-          part[j] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+          for (int j = 0; j < half * KEEP; ++j) {
+            const float give = up ? part[j] : part[j + half * KEEP], keep = up ? part[j + half * KEEP] : part[j];
+            part[j] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < KEEP; ++j) s_y[(tg + q * KEEP + j) * YS + ch] = part[j];
+        for (int j = 0; j < KEEP; ++j) s_y[(tg + q * KEEP + j) * YS + ch] = part[j];
+      }
     }
     __syncthreads();
+    if constexpr (!END) {
 #pragma unroll
-    for (int k = 0; k < NX; ++k) {
-      const int t = t0 + k * APART;
-      if (t < left && c < p.nc) {
-        auto sums = [&](int e) {
-          const float* u = &s_y[t * YS + c + e];
-          return F2{u[0], u[V > 1 ? 1 : 0]};
-        };
-        store_pack<T, V>(py + k * APART * a.y.ts, outputs<T, V>(x[k], z[k], gate, &s_D[c], sums));
+      for (int k = 0; k < NX; ++k) {
+        const int t = t0 + k * APART;
+        if (t < left && c < p.nc) {
+          auto sums = [&](int e) {
+            const float* u = &s_y[t * YS + c + e];
+            return F2{u[0], u[V > 1 ? 1 : 0]};
+          };
+          store_pack<T, V>(py + k * APART * a.y.ts, outputs<T, V>(x[k], z[k], gate, &s_D[c], sums));
+        }
       }
+      py += TT * a.y.ts;
     }
-    py += TT * a.y.ts;
   }
-  put_state(a, p, ch, q, h, a.final_state);
+  leave<END>(a, p, ch, q, h, steps);
 }
 
-// ---------------------------------------------------------------- segments
-//
-// The state that each segment begins with, in order: starts[k] arrives as the
-// end state of segment k - 1 from a zero start and leaves as
-//   starts[0] = init,  starts[k] += e^{A sums[k-1]} starts[k-1].
-// A state of 0 stays out of it: rates above 0 can make the factor infinite.
-template <typename T>
-__global__ void __launch_bounds__(256) k_selective_starts(const Args<T> a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, states = a.B * a.C * a.N;
-  if (i >= states) return;
-  const int64_t channel = i / a.N;
-  const float A2 = a.A[channel % a.C * a.N + i % a.N] * LOG2E;
-  float h = a.init ? a.init[i] : 0.f;
-  a.starts[i] = h;
-  // eight segments' loads under way together
-  constexpr int AT = 8;
-  for (int k = 1; k < a.nseg; k += AT) {
-    float sum[AT], end[AT];
-#pragma unroll
-    for (int j = 0; j < AT; ++j) {
-      const bool in = k + j < a.nseg;
-      sum[j] = in ? a.sums[(k + j - 1) * a.B * a.C + channel] : 0.f;
-      end[j] = in ? a.starts[(k + j) * states + i] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < AT; ++j) {
-      h = h == 0.f ? end[j] : fmaf(ex2(sum[j] * A2), h, end[j]);
-      if (k + j < a.nseg) a.starts[(k + j) * states + i] = h;
-    }
-  }
+// MIXED as in k_selective_teams
+template <typename T, int NS, int LPC, bool VEC, bool BVEC, bool MIXED>
+__global__ void __launch_bounds__(LANES, VEC && BVEC ? 5 : 4) k_selective_many(const Args<T> a) {
+  using S = Many<T, NS, LPC>;
+  __shared__ ManyShared<S, WORDS<T>> sh;
+  const Place<S::CB> p = place<S::CB>(a);
+  if (MIXED && p.seg > 0)
+    run_many<T, NS, LPC, VEC, BVEC, true>(a, p, sh);
+  else
+    run_many<T, NS, LPC, VEC, BVEC, false>(a, p, sh);
 }
 
 // ---------------------------------------------------------------- choice
 
-template <typename T, int NS, int LPC, bool END = false>
-cudaError_t launch_teams(Args<T> a, int64_t B, cudaStream_t st) {
+template <typename T, int NS, int LPC, bool MIXED = false>
+cudaError_t launch_teams(Args<T> a, int64_t B, cudaStream_t st, int segs = 1) {
   a.blocks_per_group = (uint32_t)ceil_div(a.per_group, LANES / LPC);
-  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group * (END ? a.nseg - 1 : a.nseg));
-  constexpr int threads = END ? LANES + HELPERS : TEAM_THREADS;
+  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group * segs);
   if constexpr (NS * LPC % (16 / (int)sizeof(T)) == 0) {
     if (a.vec && a.bvec) {
-      k_selective_teams<T, NS, LPC, true, true, END><<<blocks, threads, 0, st>>>(a);
+      k_selective_teams<T, NS, LPC, true, true, MIXED><<<blocks, TEAM_THREADS, 0, st>>>(a);
       return cudaGetLastError();
     }
   }
   if (a.vec)
-    k_selective_teams<T, NS, LPC, true, false, END><<<blocks, threads, 0, st>>>(a);
+    k_selective_teams<T, NS, LPC, true, false, MIXED><<<blocks, TEAM_THREADS, 0, st>>>(a);
   else
-    k_selective_teams<T, NS, LPC, false, false, END><<<blocks, threads, 0, st>>>(a);
+    k_selective_teams<T, NS, LPC, false, false, MIXED><<<blocks, TEAM_THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-// A few channels leave most SMs idle, and a token takes the 16-lane kernel the
-// same time however few they are: a long sequence is cut into segments that run
-// at once, first for their end states, then, from the states that these give,
-// for the outputs.  That doubles the work, so it pays up to two thirds of the
-// SMs.  The count is the one of least estimated time among those that make one,
-// two or three blocks per SM, if that is at most 0.9 of the whole's; ns per token
-// as measured (bf16, rows on 16 bytes, all or but for B and C, or not; 4096 and
-// 16384 tokens).  Whole and cut:
-// 64 channels of 1024 tokens 23 and 11 us, of 16384 tokens 323 and 34, of 65536
-// tokens 1282 and 100; 384 of 4096 83 and 44, of 1024 23 and 18; 760 of 16384
-// 332 and 250; 1024 of 16384 346 and 356 (not taken).
-struct Rates {
-  double whole, per_sm[3];
+template <typename T, int NS, int LPC, bool MIXED = false>
+cudaError_t launch_many(Args<T> a, int64_t B, cudaStream_t st, int segs = 1) {
+  a.blocks_per_group = (uint32_t)ceil_div(a.per_group, LANES / LPC);
+  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group * segs);
+  if (a.vec && a.bvec)
+    k_selective_many<T, NS, LPC, true, true, MIXED><<<blocks, LANES, 0, st>>>(a);
+  else if (a.vec)
+    k_selective_many<T, NS, LPC, true, false, MIXED><<<blocks, LANES, 0, st>>>(a);
+  else
+    k_selective_many<T, NS, LPC, false, false, MIXED><<<blocks, LANES, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+// The kernels in their forms: NS entries on each of LPC lanes.
+enum Form { T1X16, T2X8, T2X4, T4X8, T4X16, T8X16, M2X8, M4X4, M2X4, M4X8 };
+
+template <bool MIXED, typename T>
+cudaError_t launch_form(Form form, const Args<T>& a, int64_t B, cudaStream_t st, int segs) {
+  switch (form) {
+    case T2X8: return launch_teams<T, 2, 8, MIXED>(a, B, st, segs);
+    case T2X4: return launch_teams<T, 2, 4, MIXED>(a, B, st, segs);
+    case T4X8: return launch_teams<T, 4, 8, MIXED>(a, B, st, segs);
+    case T4X16: return launch_teams<T, 4, 16, MIXED>(a, B, st, segs);
+    case T8X16: return launch_teams<T, 8, 16, MIXED>(a, B, st, segs);
+    case M4X4: return launch_many<T, 4, 4, MIXED>(a, B, st, segs);
+    case M2X4: return launch_many<T, 2, 4, MIXED>(a, B, st, segs);
+    case M4X8: return launch_many<T, 4, 8, MIXED>(a, B, st, segs);
+    default: break;
+  }
+  if constexpr (!MIXED) {  // for whole sequences only
+    if (form == M2X8) return launch_many<T, 2, 8>(a, B, st, segs);
+    return launch_teams<T, 1, 16>(a, B, st, segs);
+  } else {
+    return cudaErrorInvalidValue;
+  }
+}
+
+// Whole sequences.  More lanes per channel make more warps of a small problem, at more instructions per channel, and
+// teams help where a scheduler has few warps.  The rule counts the recurrence's warps; the times are of 16 states,
+// bf16, unless said otherwise.
+inline Form whole_form(int64_t N, int64_t channels) {
+  auto warps = [&](int lpc) { return channels * lpc / 32; };
+  // 16 lanes, one entry to each: 768 channels of 2048 tokens 44 us, with 8 lanes 67 (4096 channels of 1024: 65 and
+  // 50); also for fewer entries than lanes (4 states, 770 channels of 14400 tokens: 461 us, with 4 lanes 1129)
+  if (N <= 16 && warps(16) <= 2 * SCHEDULERS) return T1X16;
+  // 8 states, 10240 channels of 1024 tokens: 81 us, with many as much (768 channels 41 and 58)
+  if (N <= 8) return T2X4;
+  if (N <= 16) {
+    // 4096 channels of 1024 tokens 50 us, with many 53 (7680 channels: 96 and 83)
+    if (warps(8) <= 2 * SCHEDULERS) return T2X8;
+    // 10240 channels of 2048 tokens 195 us, with 4 lanes 215 (40960 channels: 667 and 559)
+    return warps(8) <= 6 * SCHEDULERS ? M2X8 : M4X4;
+  }
+  // 32 states, 1024 tokens: 768 channels 51 us, with many 60 (10240 channels: 191 and 148)
+  if (N <= 32) return warps(8) <= 2 * SCHEDULERS ? T4X8 : M4X8;
+  return N <= 64 ? T4X16 : T8X16;
+}
+
+// ---------------------------------------------------------------- segments
+//
+// A token takes a form about the same time however few the blocks are, so a
+// long sequence of few channels leaves much of the GPU idle.  It is cut into
+// segments that run at once, in two launches of nseg - 1 segments each: the
+// outputs of the first with the end states of the next, then the outputs of
+// these and of the last, from the states that the first launch gives.  That
+// computes the segments between twice (their end states without outputs, which
+// costs less), and gains where the whole leaves almost half of the GPU's rate.
+// bf16, whole and cut: 64 channels of 1024 tokens 24 and 10 us, of 16384 tokens
+// 330 and 31; 1536 channels of 1024 tokens 35 and 26, of 16384 500 and 281; 5120
+// channels of 1024 73 and 66, of 16384 1114 and 899; not taken: two sequences of
+// 5120 channels (1579 us for 16384 tokens, 1528 as the best cut).
+//
+// segments() takes the form and the count of least estimated time: tokens of a
+// segment x ns per token with so many blocks per SM (as measured, bf16, rows on
+// 16 bytes, 4096 and 16384 tokens; f32 many of four entries take 1.3 times as
+// long) + 6 us and 0.1 us per segment for the launches, against the whole's and
+// 2.5 us.
+struct Rate {
+  int channels;    // of a block
+  int most, odd;   // blocks per SM, with rows on 16 bytes and without
+  double ns[5];    // per token with 1, 2, .. blocks per SM
 };
-inline int segments(const ssd_selective_dims* d, bool vec, bool bvec) {
-  if (d->dstate > 16 || d->seqlen <= 256) return 1;  // 256 tokens take 6 us: as long as the two launches more
-  static constexpr Rates ON_16{20, {19, 28, 32.5}}, X_ON_16{21.4, {27, 31.5, 1e9}}, APART{29, {35, 36, 1e9}};
-  const Rates& r = !vec ? APART : bvec ? ON_16 : X_ON_16;
-  const int64_t blocks = d->batch * d->ngroups * ceil_div(d->channels / d->ngroups, LANES / 16);
-  int best = 1;
-  double least = 0.9 * r.whole * d->seqlen;
-  for (int k = 0; k < 3; ++k) {
-    const int64_t n = std::min<int64_t>((k + 1) * 148 / blocks, MAX_SEGMENTS);
-    const double cut = 2 * r.per_sm[k] * ceil_div(d->seqlen, n < 1 ? 1 : n) + 5000 + 200 * n;
-    if (n >= 2 && cut <= least) least = cut, best = (int)n;
+constexpr Rate RATES[] = {
+    {8, 3, 2, {20.5, 30.5, 39}},   {16, 3, 2, {33, 45, 58}},            {32, 3, 2, {37, 50, 67}},
+    {16, 2, 2, {48, 69}},          {8, 2, 2, {53, 78}},                 {8, 2, 2, {80, 117}},
+    {16, 5, 4, {47, 52, 66, 76, 90}}, {32, 5, 4, {61, 76, 93, 112, 134}}, {32, 5, 4, {52, 60, 70, 82, 95}},
+    {16, 4, 4, {60, 71, 90, 107}},
+};
+struct Cut {
+  Form form;
+  int nseg;         // 1: whole sequences
+  int64_t seg_len;
+};
+inline Cut segments(const ssd_selective_dims* d, bool on_16_bytes) {
+  const int64_t N = d->dstate, L = d->seqlen, channels = d->batch * d->channels;
+  auto blocks = [&](Form f) { return d->batch * d->ngroups * ceil_div(d->channels / d->ngroups, RATES[f].channels); };
+  auto token = [&](Form f, int64_t n) {  // ns, with n blocks
+    const int most = on_16_bytes ? RATES[f].most : RATES[f].odd;
+    const int64_t per_sm = ceil_div(n, 148);
+    const double ns = per_sm / most * RATES[f].ns[most - 1] + (per_sm % most ? RATES[f].ns[per_sm % most - 1] : 0);
+    return d->io_dtype == SSD_F32 && (f == M4X4 || f == M4X8) ? 1.3 * ns : ns;
+  };
+  const Form whole = whole_form(N, channels);
+  Cut best{whole, 1, L};
+  if (L <= 256) return best;  // 6 us: the launches' own time
+  double least = 0.92 * (L * token(whole, blocks(whole)) + 2500);
+  auto consider = [&](Form f) {
+    const int most = on_16_bytes ? RATES[f].most : RATES[f].odd;
+    for (int k = 1; k <= 2 * most; ++k) {
+      const int64_t want = std::min<int64_t>(k * 148 / blocks(f) + 1, MAX_SEGMENTS);
+      const int64_t tokens = 32 * ceil_div(L, 32 * want), n = ceil_div(L, tokens);  // whole tiles
+      if (n < 3) continue;
+      const double cut = 2.0 * tokens * token(f, (n - 1) * blocks(f)) + 6000 + 100 * n;
+      if (cut <= least) least = cut, best = Cut{f, (int)n, tokens};
+    }
+  };
+  if (N <= 8) {
+    consider(T2X4), consider(M2X4);
+  } else if (N <= 16) {
+    consider(T2X8), consider(M4X4);
+  } else if (N <= 32) {
+    consider(T4X8), consider(M4X8);
+  } else {
+    consider(whole);
   }
   return best;
 }
-// starts (a multiple of 256 bytes) and sums of n segments, or 0
-inline size_t starts_bytes(const ssd_selective_dims* d, int n) {
-  return (size_t)ceil_div(n * d->batch * d->channels * d->dstate * 4, 256) * 256;
+// end states (a multiple of 256 bytes) and sums of n segments, or 0
+inline size_t ends_bytes(const ssd_selective_dims* d, int n) {
+  return (size_t)ceil_div((n - 1) * d->batch * d->channels * d->dstate * 4, 256) * 256;
 }
 inline size_t segment_bytes(const ssd_selective_dims* d, int n) {
-  return n > 1 ? starts_bytes(d, n) + (size_t)(n - 1) * d->batch * d->channels * 4 : 0;
+  return n > 1 ? ends_bytes(d, n) + (size_t)(n - 1) * d->batch * d->channels * 4 : 0;
 }
 // for rows of any alignment
 inline size_t segment_bytes(const ssd_selective_dims* d) {
-  return segment_bytes(d, std::max({segments(d, true, true), segments(d, true, false), segments(d, false, false)}));
-}
-
-template <typename T>
-cudaError_t launch_segments(const Args<T>& a, int64_t B, cudaStream_t st) {
-  cudaError_t e = launch_teams<T, 1, 16, true>(a, B, st);
-  if (e != cudaSuccess) return e;
-  k_selective_starts<T><<<(unsigned)ceil_div(B * a.C * a.N, 256), 256, 0, st>>>(a);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_teams<T, 1, 16>(a, B, st) : e;
-}
-
-template <typename T, int NS, int LPC>
-cudaError_t launch_many(Args<T> a, int64_t B, cudaStream_t st) {
-  a.blocks_per_group = (uint32_t)ceil_div(a.per_group, LANES / LPC);
-  const unsigned blocks = (unsigned)(B * a.G * a.blocks_per_group);
-  if (a.vec && a.bvec)
-    k_selective_many<T, NS, LPC, true, true><<<blocks, LANES, 0, st>>>(a);
-  else if (a.vec)
-    k_selective_many<T, NS, LPC, true, false><<<blocks, LANES, 0, st>>>(a);
-  else
-    k_selective_many<T, NS, LPC, false, false><<<blocks, LANES, 0, st>>>(a);
-  return cudaGetLastError();
+  return segment_bytes(d, std::max(segments(d, true).nseg, segments(d, false).nseg));
 }
 
 template <typename T>
@@ -771,37 +906,20 @@ cudaError_t launch_prompt(Args<T> a, int64_t B, const ssd_selective_dims* d, voi
   a.vec = a.vec && a.per_group % V == 0;
   a.bvec = a.bvec && a.N % V == 0;
   if (workspace) {
-    a.nseg = segments(d, a.vec, a.bvec);
-    a.seg_len = ceil_div(a.L, a.nseg);
-    a.starts = static_cast<float*>(workspace);
-    a.sums = a.starts + starts_bytes(d, a.nseg) / sizeof(float);
-    if (a.nseg > 1) return launch_segments(a, B, st);
+    const Cut cut = segments(d, a.vec && a.bvec);
+    if (cut.nseg > 1) {
+      a.nseg = cut.nseg;
+      a.seg_len = cut.seg_len;
+      a.ends = static_cast<float*>(workspace);
+      a.sums = a.ends + ends_bytes(d, a.nseg) / sizeof(float);
+      const cudaError_t e = launch_form<true>(cut.form, a, B, st, a.nseg - 1);
+      a.seg0 = 1;
+      return e == cudaSuccess ? launch_form<false>(cut.form, a, B, st, a.nseg - 1) : e;
+    }
   }
-  // More lanes per channel make more warps of a small problem, at more instructions per channel, and teams help where
-  // a scheduler has few warps.  The rule counts the recurrence's warps; the times are of 16 states, bf16, unless said
-  // otherwise.  In a padded batch (lengths) sequences end early and it counts half of them (five sequences, three of
-  // them with tokens, 1530 channels: 42 us with teams, 52 with many).
-  const int64_t channels = a.lengths ? ceil_div(B * a.C, 2) : B * a.C;
-  auto warps = [&](int lpc) { return channels * lpc / 32; };
-  // 16 lanes, one entry to each: 768 channels of 2048 tokens 44 us, with 8 lanes 67 (4096 channels of 1024: 65 and
-  // 50); also for fewer entries than lanes (4 states, 770 channels of 14400 tokens: 461 us, with 4 lanes 1129)
-  if (a.N <= 16 && warps(16) <= 2 * SCHEDULERS) return launch_teams<T, 1, 16>(a, B, st);
-  // 8 states, 10240 channels of 1024 tokens: 81 us, with many as much (768 channels 41 and 58)
-  if (a.N <= 8) return launch_teams<T, 2, 4>(a, B, st);
-  if (a.N <= 16) {
-    // 4096 channels of 1024 tokens 50 us, with many 53 (7680 channels: 96 and 83)
-    if (warps(8) <= 2 * SCHEDULERS) return launch_teams<T, 2, 8>(a, B, st);
-    // 10240 channels of 2048 tokens 195 us, with 4 lanes 215 (40960 channels: 667 and 559)
-    if (warps(8) <= 6 * SCHEDULERS) return launch_many<T, 2, 8>(a, B, st);
-    return launch_many<T, 4, 4>(a, B, st);
-  }
-  if (a.N <= 32) {
-    // 32 states, 1024 tokens: 768 channels 51 us, with many 60 (10240 channels: 191 and 148)
-    if (warps(8) <= 2 * SCHEDULERS) return launch_teams<T, 4, 8>(a, B, st);
-    return launch_many<T, 4, 8>(a, B, st);
-  }
-  if (a.N <= 64) return launch_teams<T, 4, 16>(a, B, st);
-  return launch_teams<T, 8, 16>(a, B, st);
+  // In a padded batch (lengths) sequences end early and half of the channels count (five sequences, three of them
+  // with tokens, 1530 channels: 42 us with teams, 52 with many).
+  return launch_form<false>(whole_form(a.N, a.lengths ? ceil_div(B * a.C, 2) : B * a.C), a, B, st, 1);
 }
 
 }  // namespace selective

@@ -481,9 +481,9 @@ typedef struct ssd_selective_dims {
 
 /*
  * Bytes of device workspace with which ssd_selective_fwd runs `d` in segments:
- * a long sequence of few channels, which would leave most SMs idle, is cut into
- * up to 64 segments that run at once (three launches: their end states, the
- * states that they begin with, their outputs).  0 where the whole sequences are
+ * a long sequence of few channels, which would leave much of the GPU idle, is
+ * cut into up to 128 segments that run at once (two launches: their end states,
+ * their outputs).  0 where the whole sequences are
  * as fast, as they are up to 256 tokens.
  */
 ssd_status ssd_selective_workspace_size(const ssd_selective_dims* d, size_t* bytes);

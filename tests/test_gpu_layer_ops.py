@@ -300,6 +300,12 @@ def test_selective_in_pieces_is_the_whole():
     (3, 1301, 65, 16, 1, (0, 0), [1301, 0, 640]),
     (2, 1024, 40, 3, 1, (0, 2), [1, 1024]),
     (4, 900, 32, 16, 1, (0, 0), None),
+    (1, 600, 64, 8, 1, (0, 0), None), (1, 1500, 400, 8, 2, (0, 0), None), (1, 1500, 401, 5, 1, (1, 0), None),
+    (1, 1500, 400, 16, 1, (0, 0), None), (1, 1500, 401, 14, 1, (1, 0), None), (2, 1400, 400, 16, 1, (0, 0), [1400, 33]),
+    (1, 1000, 64, 32, 1, (0, 0), None), (1, 1500, 400, 32, 1, (0, 0), None), (1, 1500, 400, 29, 2, (0, 0), None),
+    (1, 1000, 64, 64, 2, (0, 0), None), (1, 1000, 63, 50, 1, (1, 0), None), (1, 1000, 64, 128, 1, (0, 0), None),
+    (1, 1000, 33, 70, 1, (0, 0), None), (1, 3000, 1536, 16, 1, (0, 0), None), (1, 1500, 1001, 13, 1, (1, 0), None),
+    (1, 1500, 1601, 5, 1, (1, 0), None), (1, 1500, 1401, 29, 1, (1, 0), None), (1, 1500, 1400, 32, 1, (0, 0), None),
 ])
 def test_selective_in_segments(io, B, L, C, N, G, pad, lengths):
     """Long sequences of few channels: cut into segments, as one, and in place."""

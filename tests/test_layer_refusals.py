@@ -120,7 +120,7 @@ def test_the_binding_takes_no_host_tensors():
 
 
 def test_selective_workspace(lib):
-    """Segments where they pay: few channels, long sequences, up to 16 states."""
+    """Segments where they pay: long sequences that would not fill the GPU."""
     def size(**o):
         names = dict(batch=1, seqlen=4096, channels=64, dstate=16, ngroups=1, io=1, flags=1)
         n = ctypes.c_size_t(7)
@@ -128,15 +128,14 @@ def test_selective_workspace(lib):
         return lib.ssd_selective_workspace_size(ctypes.byref(d), ctypes.byref(n)), n.value
 
     def bytes_of(n, channels, N=16):
-        return -(-n * channels * N * 4 // 256) * 256 + (n - 1) * channels * 4
+        return -(-(n - 1) * channels * N * 4 // 256) * 256 + (n - 1) * channels * 4
 
-    # 8 blocks of 8 channels: 37 segments make two blocks for each of 148 SMs, 55 three
-    assert size() == (0, bytes_of(37, 64))
-    assert size(seqlen=512)[1] >= bytes_of(18, 64) and size(seqlen=1 << 20)[1] == bytes_of(55, 64)
-    assert size(channels=1, dstate=1, seqlen=1 << 30)[1] == bytes_of(64, 1, 1)
-    assert size(channels=384)[1] == bytes_of(9, 384)
-    assert size(channels=2048) == (0, 0) and size(batch=32) == (0, 0)   # the SMs are taken already
-    assert size(seqlen=200) == (0, 0) and size(dstate=17) == (0, 0)
+    # whole tiles of 32 tokens to a segment
+    assert size() == (0, bytes_of(32, 64)) and size(channels=1536, seqlen=16384) == (0, bytes_of(16, 1536))
+    assert size(channels=1, dstate=1, seqlen=1 << 30)[1] == bytes_of(128, 1, 1)
+    assert all(size(dstate=n)[1] > 0 for n in (1, 8, 17, 33, 64, 128))
+    assert size(channels=20480) == (0, 0) and size(batch=512) == (0, 0)   # the SMs are taken already
+    assert all(size(seqlen=n, channels=c) == (0, 0) for n in (1, 200, 256) for c in (1, 64, 1536, 5120))
     assert size(dstate=0)[0] == 2 and size(dstate=129)[0] == 5
     assert lib.ssd_selective_workspace_size(None, ctypes.byref(ctypes.c_size_t())) == 1
     assert lib.ssd_selective_workspace_size(ctypes.byref(ssd.SelectiveDims(1, 1, 1, 1, 1, 1, 0)), None) == 1
