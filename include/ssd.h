@@ -504,7 +504,8 @@ ssd_status ssd_selective_workspace_size(const ssd_selective_dims* d, size_t* byt
  *   Bm, Cm: rows of G*N entries with one pair of strides for both;
  *   init_state, final_state [B,C,N] f32 or NULL;
  *   workspace: device scratch of at least ssd_selective_workspace_size bytes,
- *   16-byte aligned, or NULL for whole sequences (the same results up to rounding).
+ *   16-byte aligned, of this call alone while it runs, or NULL for whole sequences
+ *   (the same results up to rounding).
  */
 ssd_status ssd_selective_fwd(const ssd_selective_dims* d, const void* x, int64_t x_bstride, int64_t x_tstride,
                              const void* dt, int64_t dt_bstride, int64_t dt_tstride, const float* A, const void* Bm,

@@ -70,7 +70,7 @@ def run(tiles, rng, outputs=2):
     assert not phase, "a phase is left open"
 
 
-@pytest.mark.parametrize("outputs", [2, 0])  # 0: the passes for a segment's end state have no output team
+@pytest.mark.parametrize("outputs", [2, 0])  # 0: blocks for a segment's end state have no output team
 @pytest.mark.parametrize("tiles", [0, 1, 2, 3, 4, 5, 8, 31])
 def test_no_schedule_stops_or_mixes_buffers(tiles, outputs):
     rng = random.Random(tiles)
